@@ -16,6 +16,8 @@ from ._lib import (  # noqa: F401
     bimamba_conv1d_block,
     bimamba_scan_block,
     bimamba_scan_block_workspace_bytes,
+    bimamba_scan_bwd,
+    bimamba_scan_bwd_workspace_bytes,
     bimamba_scan_fwd,
     bimamba_scan_fwd_noalloc,
     bimamba_scan_fwd_stage,

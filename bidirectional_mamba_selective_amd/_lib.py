@@ -40,6 +40,8 @@ EXPORTED = (
     "bimamba_scan_fwd_untied",
     "bimamba_scan_block_workspace_bytes",
     "bimamba_scan_block",
+    "bimamba_scan_bwd_workspace_bytes",
+    "bimamba_scan_bwd",
     "bimamba_ssd_fwd_workspace_bytes",
     "bimamba_ssd_fwd",
     "bimamba_ssd_fwd_stage",
@@ -90,6 +92,10 @@ def load() -> ctypes.CDLL:
     lib.bimamba_scan_block.restype = ctypes.c_int
     lib.bimamba_scan_block.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, ctypes.c_int,
                                        ctypes.c_uint32, vp, sz, vp]
+    lib.bimamba_scan_bwd_workspace_bytes.restype = sz
+    lib.bimamba_scan_bwd_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    lib.bimamba_scan_bwd.restype = ctypes.c_int
+    lib.bimamba_scan_bwd.argtypes = [vp] * 17 + [i64] * 4 + [ctypes.c_int, ctypes.c_uint32, vp, sz, vp]
     lib.bimamba_ssd_fwd_workspace_bytes.restype = sz
     lib.bimamba_ssd_fwd_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
     lib.bimamba_ssd_fwd.restype = ctypes.c_int
@@ -309,6 +315,59 @@ def bimamba_scan_block(x, dt, A, B, C, D=None, z=None, dt_bias=None, h_in=None, 
     if st != BIMAMBA_OK:
         raise BimambaError(st, "bimamba_scan_block")
     return out
+
+
+def bimamba_scan_bwd_workspace_bytes(batch: int, seqlen: int, d_inner: int, d_state: int) -> int:
+    return int(load().bimamba_scan_bwd_workspace_bytes(batch, seqlen, d_inner, d_state))
+
+
+def _grads(grads, shapes, device):
+    """The gradient tensors of a backward call: the caller's (grads, checked) or new ones.  shapes: name ->
+    (shape, dtype), or None for a gradient that the call does not have."""
+    torch = _torch()
+    got = {}
+    grads = grads or {}
+    unknown = [k for k, v in grads.items() if v is not None and shapes.get(k) is None]
+    if unknown:
+        raise ValueError(f"no gradient of {', '.join(sorted(unknown))} in this call")
+    for k, s in shapes.items():
+        t = grads.get(k)
+        if s is not None and t is None:
+            t = torch.empty(s[0], dtype=s[1], device=device)
+        elif s is not None:
+            _check(t, f"grads[{k!r}]", s[0], s[1], device)
+        got[k] = t
+    return got
+
+
+def bimamba_scan_bwd(dout, x, dt, A, B, C, D=None, z=None, dt_bias=None, flags: int = 0, grads=None, workspace=None,
+                     stream=None):
+    """Gradients of bimamba_scan_fwd's inputs for the gradient dout of its output; the other arguments and the flags
+    are those of the forward call.  Returns a dict with keys x, dt, A, B, C, D, z, dt_bias: tensors like those
+    inputs, None for an optional input that was not given.  grads may hold tensors to write into."""
+    torch = _torch()
+    lib = load()
+    if x.dim() != 3:
+        raise ValueError("x must be [batch, seqlen, d_inner]")
+    with torch.cuda.device(x.device), _on(stream):
+        nb, L, nd, ns, dout = _common(x, dt, A, B, C, D, z, dt_bias, dout)
+        gated = not flags & FLAG_NO_GATE
+        f32 = torch.float32
+        g = _grads(grads, {"x": (x.shape, x.dtype), "dt": (x.shape, x.dtype), "A": (A.shape, f32),
+                           "B": (B.shape, x.dtype), "C": (C.shape, x.dtype),
+                           "D": ((nd,), f32) if D is not None else None, "z": (x.shape, x.dtype) if gated else None,
+                           "dt_bias": ((nd,), f32) if dt_bias is not None else None}, x.device)
+        if workspace is None:
+            need = int(lib.bimamba_scan_bwd_workspace_bytes(nb, L, nd, ns))
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
+        st = lib.bimamba_scan_bwd(_ptr(dout), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+                                  _ptr(dt_bias), _ptr(g["x"]), _ptr(g["dt"]), _ptr(g["A"]), _ptr(g["B"]),
+                                  _ptr(g["C"]), _ptr(g["D"]), _ptr(g["z"]), _ptr(g["dt_bias"]), nb, L, nd, ns,
+                                  _io_dtype(x), flags, _ptr(workspace), _nbytes(workspace, x.device),
+                                  _stream(stream, x.device))
+    if st != BIMAMBA_OK:
+        raise BimambaError(st, "bimamba_scan_bwd")
+    return g
 
 
 def bimamba_ssd_fwd_workspace_bytes(batch: int, seqlen: int, nheads: int, headdim: int, d_state: int) -> int:

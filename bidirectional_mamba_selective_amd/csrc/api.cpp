@@ -6,6 +6,7 @@
 
 #include <algorithm>
 
+#include "bwd_plan.h"
 #include "launch.h"
 #include "plan.h"
 
@@ -516,6 +517,76 @@ int bimamba_conv1d_block(const void* u, const float* w_f, const float* b_f, cons
                          hipStream_t stream) {
   return conv_impl(u, w_f, b_f, w_r, b_r, cache_in, cache_out, out_f, out_r, batch, block_len, channels, d_conv,
                    io_dtype, flags, stream, true);
+}
+
+// ---- Backward pass of the scan ----
+
+namespace {
+
+// One buffer of a call: where it lies (no bytes: absent) and the alignment it needs.
+struct Buf {
+  const void* p;
+  size_t bytes;
+  uintptr_t align;
+};
+
+// Every present buffer aligned, and no output (the first nout) overlapping any other buffer.
+bool buffers_ok(const Buf* v, int n, int nout) {
+  for (int i = 0; i < n; ++i) {
+    if (!v[i].p) continue;
+    if (!aligned(v[i].p, v[i].align)) return false;
+    for (int j = 0; j < i && j < nout; ++j)
+      if (v[j].p && overlap(range_of(v[i].p, v[i].bytes), range_of(v[j].p, v[j].bytes))) return false;
+  }
+  return true;
+}
+
+// The launches of the backward pass run one thread per (tile token, state) of B and C together, per (batch element,
+// state, channel), and per channel and row of the parameter gradients; a launch holds fewer than 2^32 threads.
+int check_bwd_shape(int64_t batch, int64_t seqlen, int64_t d_inner, int64_t d_state, int io_dtype) {
+  const int s = check_shape(batch, seqlen, d_inner, d_state, io_dtype);
+  if (s != BIMAMBA_OK) return s;
+  const double rows = static_cast<double>(batch) * ((seqlen + bimamba::kSub - 1) / bimamba::kSub * bimamba::kSub);
+  if (rows * d_state * 2 + static_cast<double>(d_state + 2) * d_inner * 4 + 1024 > 4294967295.0 ||
+      static_cast<double>(batch) * d_state * d_inner + 256 > 4294967295.0)
+    return BIMAMBA_ERR_UNSUPPORTED;
+  return BIMAMBA_OK;
+}
+
+}  // namespace
+
+size_t bimamba_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, int64_t d_state) {
+  if (check_bwd_shape(batch, seqlen, d_inner, d_state, BIMAMBA_BF16) != BIMAMBA_OK) return 0;
+  return bimamba::make_bwd_plan(batch, seqlen, d_inner, d_state).total;
+}
+
+int bimamba_scan_bwd(const void* dout, const void* x, const void* dt, const float* A, const void* B, const void* C,
+                     const float* D, const void* z, const float* dt_bias, void* dx, void* ddt, float* dA, void* dB,
+                     void* dC, float* dD, void* dz, float* ddt_bias, int64_t batch, int64_t seqlen, int64_t d_inner,
+                     int64_t d_state, int io_dtype, uint32_t flags, void* workspace, size_t workspace_bytes,
+                     hipStream_t stream) {
+  int s = check_bwd_shape(batch, seqlen, d_inner, d_state, io_dtype);
+  if (s != BIMAMBA_OK) return s;
+  if (flags & ~kKnownFlags) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  if ((flags & BIMAMBA_FLAG_FWD_ONLY) && (flags & BIMAMBA_FLAG_REV_ONLY)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  if (!dout || !x || !dt || !A || !B || !C || !dx || !ddt || !dA || !dB || !dC) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const bool gate = !(flags & BIMAMBA_FLAG_NO_GATE);
+  if (gate ? !z || !dz : dz != nullptr) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const size_t es = io_dtype == BIMAMBA_BF16 ? 2 : 4;
+  const size_t act = static_cast<size_t>(batch) * seqlen * d_inner * es;
+  const size_t bc = static_cast<size_t>(batch) * seqlen * d_state * es;
+  const size_t par = static_cast<size_t>(d_inner) * d_state * 4, vec = static_cast<size_t>(d_inner) * 4;
+  const bimamba::BwdPlan p = bimamba::make_bwd_plan(batch, seqlen, d_inner, d_state);
+  if (workspace_bytes < p.total) return BIMAMBA_ERR_WORKSPACE_TOO_SMALL;
+  if (!workspace) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const Buf v[] = {{dx, act, 16},  {ddt, act, 16},      {dA, par, 16},        {dB, bc, es},    {dC, bc, es},
+                   {dD, vec, 16},  {dz, act, 16},       {ddt_bias, vec, 16},  {workspace, p.total, 256},
+                   {dout, act, 16}, {x, act, 16},       {dt, act, 16},        {A, par, 16},    {B, bc, es},
+                   {C, bc, es},    {D, vec, 16},        {gate ? z : nullptr, act, 16}, {dt_bias, vec, 16}};
+  if (!buffers_ok(v, static_cast<int>(sizeof(v) / sizeof(v[0])), 9)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const bimamba::ScanBwdArgs a{dout, x,  dt, A,  B,  C,  D,        gate ? z : nullptr, dt_bias, dx,
+                               ddt,  dA, dB, dC, dD, dz, ddt_bias, io_dtype,           flags};
+  return map_hip(bimamba::launch_scan_bwd(a, p, workspace, stream));
 }
 
 }  // extern "C"

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "bwd_plan.h"
 #include "plan.h"
 #include "ssd_plan.h"
 
@@ -42,6 +43,31 @@ hipError_t scratch_address(void** out);
 // (16 channels, batch element), one lane per (channel, state) recurrence; no workspace.
 hipError_t launch_block_fused(const ScanArgs& a, int64_t batch, int64_t block_len, int64_t d_inner,
                               int64_t d_state, hipStream_t stream);
+
+// Backward pass of the scan: gradients of every input of ScanArgs for the gradient dout of out.
+struct ScanBwdArgs {
+  const void* dout;
+  const void* x;
+  const void* dt;
+  const float* A;
+  const void* B;
+  const void* C;
+  const float* D;
+  const void* z;
+  const float* dt_bias;
+  void* dx;
+  void* ddt;
+  float* dA;
+  void* dB;
+  void* dC;
+  float* dD;        // null = not written
+  void* dz;         // null without the gate
+  float* ddt_bias;  // null = not written
+  int io_dtype;
+  uint32_t flags;
+};
+
+hipError_t launch_scan_bwd(const ScanBwdArgs& a, const BwdPlan& p, void* workspace, hipStream_t stream);
 
 namespace conv {
 

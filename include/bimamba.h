@@ -181,6 +181,44 @@ int bimamba_scan_block(const void* x, const void* dt, const float* A, const void
                        int io_dtype, uint32_t flags, void* workspace, size_t workspace_bytes,
                        hipStream_t stream);
 
+/* Bytes of device workspace bimamba_scan_bwd needs for this shape (a pure host
+ * computation, no HIP call).  Returns 0 for an unsupported shape. */
+size_t bimamba_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, int64_t d_state);
+
+/* Backward pass of bimamba_scan_fwd: given dout, the gradient of a loss with
+ * respect to out ([batch, seqlen, d_inner], io_dtype), the gradients with
+ * respect to every input, summed over the directions the flags keep.  Nothing
+ * of the forward call is needed: the states are recomputed from its inputs.
+ * With dy = dout * silu(z) (dy = dout with NO_GATE), k the number of directions
+ * kept, and the adjoints, which run against their direction,
+ *   gf[t] = C[t,n] dy[t,d] + abar[t+1] gf[t+1],   gr[t] = C[t,n] dy[t,d] + abar[t-1] gr[t-1]
+ *   w[t]  = abar[t] * (gf[t] h_fwd[t-1] + gr[t] h_rev[t+1])
+ * the gradients are
+ *   dB[t,n] = sum_d delta x (gf + gr)         dC[t,n] = sum_d dy (h_fwd + h_rev)
+ *   dx      = delta * sum_n B (gf + gr) + k D dy
+ *   ddt     = sigmoid(dt + dt_bias) * (x sum_n B (gf + gr) + sum_n A[d,n] w)
+ *   dA[d,n] = sum_t delta w        ddt_bias[d] = sum_t ddt      dD[d] = sum_t k x dy
+ *   dz      = dout * y * silu'(z),  y the forward pass's sum before the gate
+ * Untied directions (bimamba_scan_fwd_untied) are two calls, one with FWD_ONLY on
+ * set f and out_f's gradient, one with REV_ONLY on set r and out_r's.
+ *   dx, ddt, dz: like x; dB, dC: like B (io_dtype, rounded to nearest even from
+ *   fp32 sums); dA [d_inner, d_state], dD, ddt_bias [d_inner]: fp32.  Sums over
+ *   tokens, batch and channels are taken in fp32 in a fixed order: two calls on
+ *   the same inputs give the same bits.
+ * dD and ddt_bias may be NULL (not written); they may be asked for also where D
+ * or dt_bias is NULL (= 0).  dz is required with the gate and must be NULL with
+ * NO_GATE (z is then not read).  Shapes, dtypes, alignment (dA, dD, ddt_bias, dx,
+ * ddt, dz 16 bytes; dB, dC one element) and the workspace (256-byte aligned,
+ * contents ignored on entry) are as for bimamba_scan_fwd, and batch * d_state *
+ * (seqlen rounded up to 16) must stay below 2^31 and batch * d_state * d_inner below
+ * 2^32 (UNSUPPORTED otherwise).  No output may overlap an input, another output or
+ * the workspace. */
+int bimamba_scan_bwd(const void* dout, const void* x, const void* dt, const float* A, const void* B, const void* C,
+                     const float* D, const void* z, const float* dt_bias, void* dx, void* ddt, float* dA, void* dB,
+                     void* dC, float* dD, void* dz, float* ddt_bias, int64_t batch, int64_t seqlen, int64_t d_inner,
+                     int64_t d_state, int io_dtype, uint32_t flags, void* workspace, size_t workspace_bytes,
+                     hipStream_t stream);
+
 /* ---- Mamba-2 (SSD) heads ------------------------------------------------
  * The mixer the paper actually runs is a bidirectional Mamba-2 layer (Section
  * 1; Appendix A Table 7: SSM head size 32 and state size 128; Appendix C
