@@ -11,8 +11,14 @@ from ._lib import (  # noqa: F401
     FLAG_NO_SILU,
     FLAG_NO_GATE,
     FLAG_REV_ONLY,
+    FLAG_RMS_NORM,
     BimambaError,
+    bimamba_adaln_bwd,
+    bimamba_adaln_bwd_workspace_bytes,
+    bimamba_adaln_fwd,
     bimamba_conv1d_bidir,
+    bimamba_conv1d_bidir_bwd,
+    bimamba_conv1d_bidir_bwd_workspace_bytes,
     bimamba_conv1d_block,
     bimamba_scan_block,
     bimamba_scan_block_workspace_bytes,

@@ -28,6 +28,7 @@ FLAG_NO_GATE = 1
 FLAG_FWD_ONLY = 2
 FLAG_REV_ONLY = 4
 FLAG_NO_SILU = 16
+FLAG_RMS_NORM = 32
 
 # every symbol include/bimamba.h declares
 EXPORTED = (
@@ -50,6 +51,11 @@ EXPORTED = (
     "bimamba_ssd_conv_untied",
     "bimamba_conv1d_bidir",
     "bimamba_conv1d_block",
+    "bimamba_conv1d_bidir_bwd_workspace_bytes",
+    "bimamba_conv1d_bidir_bwd",
+    "bimamba_adaln_fwd",
+    "bimamba_adaln_bwd_workspace_bytes",
+    "bimamba_adaln_bwd",
 )
 
 _lib = None
@@ -113,6 +119,17 @@ def load() -> ctypes.CDLL:
     lib.bimamba_conv1d_bidir.argtypes = [vp] * 7 + [i64] * 4 + [ctypes.c_int, ctypes.c_uint32, vp]
     lib.bimamba_conv1d_block.restype = ctypes.c_int
     lib.bimamba_conv1d_block.argtypes = [vp] * 9 + [i64] * 4 + [ctypes.c_int, ctypes.c_uint32, vp]
+    lib.bimamba_conv1d_bidir_bwd_workspace_bytes.restype = sz
+    lib.bimamba_conv1d_bidir_bwd_workspace_bytes.argtypes = [i64] * 3
+    lib.bimamba_conv1d_bidir_bwd.restype = ctypes.c_int
+    lib.bimamba_conv1d_bidir_bwd.argtypes = [vp] * 12 + [i64] * 4 + [ctypes.c_int, ctypes.c_uint32, vp, sz, vp]
+    lib.bimamba_adaln_fwd.restype = ctypes.c_int
+    lib.bimamba_adaln_fwd.argtypes = [vp] * 8 + [i64] * 4 + [ctypes.c_float, ctypes.c_int, ctypes.c_uint32, vp]
+    lib.bimamba_adaln_bwd_workspace_bytes.restype = sz
+    lib.bimamba_adaln_bwd_workspace_bytes.argtypes = [i64] * 3
+    lib.bimamba_adaln_bwd.restype = ctypes.c_int
+    lib.bimamba_adaln_bwd.argtypes = [vp] * 13 + [i64] * 4 + [ctypes.c_float, ctypes.c_int, ctypes.c_uint32, vp, sz,
+                                                              vp]
     _lib = lib
     return lib
 
@@ -570,3 +587,111 @@ def bimamba_conv1d_block(u, w_f=None, b_f=None, w_r=None, b_r=None, cache_in=Non
     if st != BIMAMBA_OK:
         raise BimambaError(st, "bimamba_conv1d_block")
     return out_f, out_r
+
+
+def bimamba_conv1d_bidir_bwd_workspace_bytes(batch: int, seqlen: int, channels: int) -> int:
+    return int(load().bimamba_conv1d_bidir_bwd_workspace_bytes(batch, seqlen, channels))
+
+
+def bimamba_conv1d_bidir_bwd(dout_f, dout_r, u, w_f=None, b_f=None, w_r=None, b_r=None, flags: int = 0, grads=None,
+                             workspace=None, stream=None):
+    """Gradients of bimamba_conv1d_bidir's inputs for the gradients dout_f, dout_r of its outputs (None: that direction
+    is left out).  Returns a dict with keys u, w_f, b_f, w_r, b_r, None for what a left-out direction or a missing bias
+    does not have.  grads may hold tensors to write into."""
+    torch = _torch()
+    lib = load()
+    for d, w, b, name in ((dout_f, w_f, b_f, "f"), (dout_r, w_r, b_r, "r")):
+        if (d is None) != (w is None):
+            raise ValueError(f"dout_{name} and w_{name} come together")
+        if d is None and b is not None:
+            raise ValueError(f"b_{name} without dout_{name}")
+    with torch.cuda.device(u.device), _on(stream):
+        # the gradients of the outputs have the outputs' shapes
+        nb, L, nc, K, dout_f, dout_r = _conv_common(u, w_f, b_f, w_r, b_r, dout_f, dout_r)
+        f32 = torch.float32
+        g = _grads(grads, {"u": (u.shape, u.dtype), **{k: None if t is None else (t.shape, f32) for k, t in
+                                                        (("w_f", w_f), ("b_f", b_f), ("w_r", w_r), ("b_r", b_r))}},
+                   u.device)
+        if workspace is None:
+            need = int(lib.bimamba_conv1d_bidir_bwd_workspace_bytes(nb, L, nc))
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=u.device)
+        st = lib.bimamba_conv1d_bidir_bwd(_ptr(dout_f), _ptr(dout_r), _ptr(u), _ptr(w_f), _ptr(b_f), _ptr(w_r),
+                                          _ptr(b_r), _ptr(g["u"]), _ptr(g["w_f"]), _ptr(g["b_f"]), _ptr(g["w_r"]),
+                                          _ptr(g["b_r"]), nb, L, nc, K, _io_dtype(u), flags, _ptr(workspace),
+                                          _nbytes(workspace, u.device), _stream(stream, u.device))
+    if st != BIMAMBA_OK:
+        raise BimambaError(st, "bimamba_conv1d_bidir_bwd")
+    return g
+
+
+def _adaln_common(x, name, gamma, beta, branch, post_weight, gate):
+    torch = _torch()
+    if x.dim() != 3:
+        raise ValueError(f"{name} must be [batch, seqlen, d_model]")
+    nb, L, nd = x.shape
+    mods = [(k, t) for k, t in (("gamma", gamma), ("beta", beta), ("gate", gate)) if t is not None]
+    rows = mods[0][1].shape[0] if mods and mods[0][1].dim() == 2 else nb
+    if rows not in (1, nb):
+        raise ValueError(f"{mods[0][0]} must have one row, or one per sequence")
+    for k, t in mods:
+        _check(t, k, (rows, nd), torch.float32, x.device)
+    _check(x, name, (nb, L, nd), x.dtype, x.device)
+    _check(branch, "branch", (nb, L, nd), x.dtype, x.device)
+    _check(post_weight, "post_weight", (nd,), torch.float32, x.device)
+    return nb, L, nd, rows
+
+
+def bimamba_adaln_fwd(x, gamma=None, beta=None, branch=None, post_weight=None, gate=None, eps: float = 1e-5,
+                      flags: int = 0, h=None, out=None, stream=None):
+    """The step between two blocks: h = x + gate * (RMSNorm(branch) * post_weight), out = gamma * LayerNorm(h) + beta
+    (FLAG_RMS_NORM: RMSNorm).  gamma, beta, gate are [batch, d_model] or [1, d_model] fp32.  Returns (h, out); without a
+    branch h is x.  h may be given as x to update the residual stream in place."""
+    torch = _torch()
+    lib = load()
+    with torch.cuda.device(x.device), _on(stream):
+        nb, L, nd, rows = _adaln_common(x, "x", gamma, beta, branch, post_weight, gate)
+        if branch is not None and h is None:
+            h = torch.empty_like(x)
+        if out is None:
+            out = torch.empty_like(x)
+        _check(h, "h", x.shape, x.dtype, x.device)
+        _check(out, "out", x.shape, x.dtype, x.device)
+        st = lib.bimamba_adaln_fwd(_ptr(x), _ptr(branch), _ptr(post_weight), _ptr(gate), _ptr(gamma), _ptr(beta),
+                                   _ptr(h), _ptr(out), nb, L, nd, rows, eps, _io_dtype(x), flags,
+                                   _stream(stream, x.device))
+    if st != BIMAMBA_OK:
+        raise BimambaError(st, "bimamba_adaln_fwd")
+    return (x if branch is None else h), out
+
+
+def bimamba_adaln_bwd_workspace_bytes(batch: int, seqlen: int, d_model: int) -> int:
+    return int(load().bimamba_adaln_bwd_workspace_bytes(batch, seqlen, d_model))
+
+
+def bimamba_adaln_bwd(dout, dres, h, gamma=None, beta=None, branch=None, post_weight=None, gate=None,
+                      eps: float = 1e-5, flags: int = 0, grads=None, workspace=None, stream=None):
+    """Gradients of bimamba_adaln_fwd's inputs, from dout (of out), dres (of h, None = 0) and the forward call's h (x
+    where it had no branch).  Returns a dict with keys x, gamma, beta, branch, post_weight, gate, None for an input
+    that was not given.  grads may hold tensors to write into; grads["x"] may be dres."""
+    torch = _torch()
+    lib = load()
+    with torch.cuda.device(h.device), _on(stream):
+        nb, L, nd, rows = _adaln_common(h, "h", gamma, beta, branch, post_weight, gate)
+        _check(dout, "dout", h.shape, h.dtype, h.device)
+        _check(dres, "dres", h.shape, h.dtype, h.device)
+        f32 = torch.float32
+        g = _grads(grads, {"x": (h.shape, h.dtype), "branch": None if branch is None else (h.shape, h.dtype),
+                           **{k: None if t is None else (t.shape, f32) for k, t in
+                              (("gamma", gamma), ("beta", beta), ("post_weight", post_weight), ("gate", gate))}},
+                   h.device)
+        if workspace is None:
+            need = int(lib.bimamba_adaln_bwd_workspace_bytes(nb, L, nd))
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=h.device)
+        st = lib.bimamba_adaln_bwd(_ptr(dout), _ptr(dres), _ptr(h), _ptr(branch), _ptr(post_weight), _ptr(gate),
+                                   _ptr(gamma), _ptr(g["x"]), _ptr(g["branch"]), _ptr(g["post_weight"]),
+                                   _ptr(g["gate"]), _ptr(g["gamma"]), _ptr(g["beta"]), nb, L, nd, rows, eps,
+                                   _io_dtype(h), flags, _ptr(workspace), _nbytes(workspace, h.device),
+                                   _stream(stream, h.device))
+    if st != BIMAMBA_OK:
+        raise BimambaError(st, "bimamba_adaln_bwd")
+    return g

@@ -1,0 +1,52 @@
+// Host-side decomposition of the norm / gate / residual step: rows of d_model
+// values over workgroups, and the layout of the backward pass's workspace.
+// Pure host code: no HIP calls.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "plan.h"
+
+namespace bimamba {
+namespace adaln {
+
+constexpr int64_t kVec = 8;           // values per thread and vector load
+constexpr int64_t kMaxWidth = 8192;   // widest row: 16 wavefronts, one vector per lane
+constexpr int64_t kFwdGroups = 2048;  // workgroups the forward pass aims at (8 per CU)
+constexpr int64_t kBwdGroups = 1024;  // the backward pass: 4 per CU (its partial sums grow with them)
+constexpr int kSums = 4;              // column sums of the backward pass: dgamma, dbeta, dgate, dpost_weight
+
+// Wavefronts per row, one vector per lane.  A row of up to 512 values stays in one wavefront, and its sums need no
+// barrier.
+inline int waves_for(int64_t d) {
+  int w = 1;
+  while (w * 64 * kVec < d) w *= 2;
+  return w;
+}
+
+// Rows a workgroup holds at once.
+inline int row_groups(int waves) { return waves == 1 ? 4 : 1; }
+
+struct Plan {
+  int waves;
+  int64_t rows_per_wg;  // consecutive rows of one batch element
+  int64_t chunks;       // workgroups per batch element
+  size_t part_bytes;    // backward: partial column sums [batch][chunk][row group][kSums][d] fp32
+};
+
+inline Plan make_plan(int64_t batch, int64_t seqlen, int64_t d, int64_t want_groups) {
+  Plan p{};
+  p.waves = waves_for(d);
+  const int64_t g = row_groups(p.waves);
+  int64_t per_batch = (want_groups + batch - 1) / batch;
+  int64_t rows = (seqlen + per_batch - 1) / per_batch;
+  rows = (rows + g - 1) / g * g;
+  p.rows_per_wg = rows;
+  p.chunks = (seqlen + rows - 1) / rows;
+  p.part_bytes = align256(static_cast<size_t>(batch) * p.chunks * g * kSums * d * sizeof(float));
+  return p;
+}
+
+}  // namespace adaln
+}  // namespace bimamba

@@ -5,8 +5,11 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 
+#include "adaln_plan.h"
 #include "bwd_plan.h"
+#include "conv_bwd_plan.h"
 #include "launch.h"
 #include "plan.h"
 
@@ -587,6 +590,123 @@ int bimamba_scan_bwd(const void* dout, const void* x, const void* dt, const floa
   const bimamba::ScanBwdArgs a{dout, x,  dt, A,  B,  C,  D,        gate ? z : nullptr, dt_bias, dx,
                                ddt,  dA, dB, dC, dD, dz, ddt_bias, io_dtype,           flags};
   return map_hip(bimamba::launch_scan_bwd(a, p, workspace, stream));
+}
+
+// ---- Backward pass of the short convolution ----
+
+static int conv_bwd_check_shape(int64_t batch, int64_t L, int64_t C, int64_t d_conv, int io_dtype) {
+  if (batch <= 0 || L <= 0 || C <= 0 || d_conv <= 0) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  if (io_dtype != BIMAMBA_F32 && io_dtype != BIMAMBA_BF16) return BIMAMBA_ERR_UNSUPPORTED;
+  if (d_conv != 4 || C % 4 != 0 || C > (int64_t{1} << 22)) return BIMAMBA_ERR_UNSUPPORTED;
+  if (batch > 65535 || L > INT32_MAX / 2) return BIMAMBA_ERR_UNSUPPORTED;
+  const bimamba::conv::BwdPlan p = bimamba::conv::make_conv_bwd_plan(batch, L, C);
+  // a launch holds fewer than 2^32 threads
+  if (static_cast<double>(p.groups) * p.cblocks * 64 * bimamba::conv::kBwdWaves > 4294967295.0)
+    return BIMAMBA_ERR_UNSUPPORTED;
+  return BIMAMBA_OK;
+}
+
+size_t bimamba_conv1d_bidir_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t channels) {
+  if (conv_bwd_check_shape(batch, seqlen, channels, 4, BIMAMBA_F32) != BIMAMBA_OK) return 0;
+  return bimamba::conv::make_conv_bwd_plan(batch, seqlen, channels).total;
+}
+
+int bimamba_conv1d_bidir_bwd(const void* dout_f, const void* dout_r, const void* u, const float* w_f, const float* b_f,
+                             const float* w_r, const float* b_r, void* du, float* dw_f, float* db_f, float* dw_r,
+                             float* db_r, int64_t batch, int64_t seqlen, int64_t channels, int64_t d_conv, int io_dtype,
+                             uint32_t flags, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const int s = conv_bwd_check_shape(batch, seqlen, channels, d_conv, io_dtype);
+  if (s != BIMAMBA_OK) return s;
+  if (flags & ~static_cast<uint32_t>(BIMAMBA_FLAG_NO_SILU)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  if (!u || !du || (!dout_f && !dout_r)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  if (dout_f ? !w_f || !dw_f : dw_f || db_f) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  if (dout_r ? !w_r || !dw_r : dw_r || db_r) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const bimamba::conv::BwdPlan p = bimamba::conv::make_conv_bwd_plan(batch, seqlen, channels);
+  if (workspace_bytes < p.total) return BIMAMBA_ERR_WORKSPACE_TOO_SMALL;
+  if (!workspace) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const size_t es = io_dtype == BIMAMBA_BF16 ? 2 : 4;
+  const size_t act = static_cast<size_t>(batch) * seqlen * channels * es;
+  const size_t wb = static_cast<size_t>(channels) * 16, bb = static_cast<size_t>(channels) * 4;
+  const Buf v[] = {{du, act, 4 * es}, {dw_f, wb, 4}, {db_f, bb, 4}, {dw_r, wb, 4}, {db_r, bb, 4},
+                   {workspace, p.total, 256}, {dout_f, act, 4 * es}, {dout_r, act, 4 * es}, {u, act, 4 * es},
+                   // the parameters of a direction that is left out are not read
+                   {dout_f ? w_f : nullptr, wb, 4}, {dout_f ? b_f : nullptr, bb, 4},
+                   {dout_r ? w_r : nullptr, wb, 4}, {dout_r ? b_r : nullptr, bb, 4}};
+  if (!buffers_ok(v, static_cast<int>(sizeof(v) / sizeof(v[0])), 6)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const bimamba::conv::ConvBwdArgs a{dout_f, dout_r, u, w_f, b_f, w_r, b_r, du, dw_f, db_f, dw_r, db_r,
+                                     (flags & BIMAMBA_FLAG_NO_SILU) ? 0 : 1};
+  return map_hip(bimamba::conv::launch_conv_bwd(a, p, batch, seqlen, channels, io_dtype, workspace, stream));
+}
+
+// ---- Norm, gate and residual between two blocks ----
+
+static int adaln_check_shape(int64_t batch, int64_t seqlen, int64_t d_model, int io_dtype) {
+  if (batch <= 0 || seqlen <= 0 || d_model <= 0) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  if (io_dtype != BIMAMBA_F32 && io_dtype != BIMAMBA_BF16) return BIMAMBA_ERR_UNSUPPORTED;
+  if (d_model % bimamba::adaln::kVec != 0 || d_model > bimamba::adaln::kMaxWidth) return BIMAMBA_ERR_UNSUPPORTED;
+  if (batch > 65535 || static_cast<double>(batch) * seqlen * d_model > 9.0e15) return BIMAMBA_ERR_UNSUPPORTED;
+  return BIMAMBA_OK;
+}
+
+// What the forward and the backward call have in common.
+static int adaln_check(const void* branch, const float* post_weight, const float* gate, int64_t batch, int64_t seqlen,
+                       int64_t d_model, int64_t mod_rows, float eps, int io_dtype, uint32_t flags) {
+  const int s = adaln_check_shape(batch, seqlen, d_model, io_dtype);
+  if (s != BIMAMBA_OK) return s;
+  if (mod_rows != 1 && mod_rows != batch) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  if (flags & ~static_cast<uint32_t>(BIMAMBA_FLAG_RMS_NORM)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  if (!branch && (post_weight || gate)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  return BIMAMBA_OK;
+}
+
+int bimamba_adaln_fwd(const void* x, const void* branch, const float* post_weight, const float* gate,
+                      const float* gamma, const float* beta, void* h, void* out, int64_t batch, int64_t seqlen,
+                      int64_t d_model, int64_t mod_rows, float eps, int io_dtype, uint32_t flags, hipStream_t stream) {
+  const int s = adaln_check(branch, post_weight, gate, batch, seqlen, d_model, mod_rows, eps, io_dtype, flags);
+  if (s != BIMAMBA_OK) return s;
+  if (!x || !out || (branch != nullptr) != (h != nullptr)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const size_t act = static_cast<size_t>(batch) * seqlen * d_model * (io_dtype == BIMAMBA_BF16 ? 2 : 4);
+  const size_t mod = static_cast<size_t>(mod_rows) * d_model * 4, vec = static_cast<size_t>(d_model) * 4;
+  // h may be x itself: every value of x is read before the h of its row is written, by the lane that writes it
+  if (!aligned(x, 16)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const Buf v[] = {{h, act, 16}, {out, act, 16}, {h == x ? nullptr : x, act, 16}, {branch, act, 16},
+                   {post_weight, vec, 16}, {gate, mod, 16}, {gamma, mod, 16}, {beta, mod, 16}};
+  if (!buffers_ok(v, static_cast<int>(sizeof(v) / sizeof(v[0])), 2)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const bimamba::adaln::AdalnArgs a{x, branch, post_weight, gate, gamma, beta, h, out, batch, seqlen, d_model,
+                                    mod_rows, eps, (flags & BIMAMBA_FLAG_RMS_NORM) ? 1 : 0, io_dtype};
+  return map_hip(bimamba::adaln::launch_adaln_fwd(a, stream));
+}
+
+size_t bimamba_adaln_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t d_model) {
+  if (adaln_check_shape(batch, seqlen, d_model, BIMAMBA_F32) != BIMAMBA_OK) return 0;
+  return bimamba::adaln::make_plan(batch, seqlen, d_model, bimamba::adaln::kBwdGroups).part_bytes;
+}
+
+int bimamba_adaln_bwd(const void* dout, const void* dres, const void* h, const void* branch, const float* post_weight,
+                      const float* gate, const float* gamma, void* dx, void* dbranch, float* dpost_weight,
+                      float* dgate, float* dgamma, float* dbeta, int64_t batch, int64_t seqlen, int64_t d_model,
+                      int64_t mod_rows, float eps, int io_dtype, uint32_t flags, void* workspace,
+                      size_t workspace_bytes, hipStream_t stream) {
+  const int s = adaln_check(branch, post_weight, gate, batch, seqlen, d_model, mod_rows, eps, io_dtype, flags);
+  if (s != BIMAMBA_OK) return s;
+  if (!dout || !h || !dx || (branch != nullptr) != (dbranch != nullptr)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  if ((dgate && !branch) || (dpost_weight && !post_weight)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const size_t need = bimamba_adaln_bwd_workspace_bytes(batch, seqlen, d_model);
+  if (workspace_bytes < need) return BIMAMBA_ERR_WORKSPACE_TOO_SMALL;
+  if (!workspace || (dres && !aligned(dres, 16))) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const size_t act = static_cast<size_t>(batch) * seqlen * d_model * (io_dtype == BIMAMBA_BF16 ? 2 : 4);
+  const size_t mod = static_cast<size_t>(mod_rows) * d_model * 4, vec = static_cast<size_t>(d_model) * 4;
+  // dx may be dres itself, as h may be x in the forward call
+  const Buf v[] = {{dx, act, 16}, {dbranch, act, 16}, {dpost_weight, vec, 16}, {dgate, mod, 16}, {dgamma, mod, 16},
+                   {dbeta, mod, 16}, {workspace, need, 256}, {dout, act, 16}, {dres == dx ? nullptr : dres, act, 16},
+                   {h, act, 16}, {branch, act, 16}, {post_weight, vec, 16}, {gate, mod, 16}, {gamma, mod, 16}};
+  if (!buffers_ok(v, static_cast<int>(sizeof(v) / sizeof(v[0])), 7)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const bimamba::adaln::AdalnArgs a{nullptr, branch, post_weight, gate, gamma, nullptr, const_cast<void*>(h), nullptr,
+                                    batch, seqlen, d_model, mod_rows, eps, (flags & BIMAMBA_FLAG_RMS_NORM) ? 1 : 0,
+                                    io_dtype};
+  const bimamba::adaln::AdalnGrads g{dout, dres, dx, dbranch, dpost_weight, dgate, dgamma, dbeta};
+  return map_hip(bimamba::adaln::launch_adaln_bwd(a, g, workspace, stream));
 }
 
 }  // extern "C"

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "bwd_plan.h"
+#include "conv_bwd_plan.h"
 #include "plan.h"
 #include "ssd_plan.h"
 
@@ -69,6 +70,40 @@ struct ScanBwdArgs {
 
 hipError_t launch_scan_bwd(const ScanBwdArgs& a, const BwdPlan& p, void* workspace, hipStream_t stream);
 
+namespace adaln {
+
+// The norm / gate / residual step between two blocks; null pointers as in the C ABI.
+struct AdalnArgs {
+  const void* x;  // forward only
+  const void* branch;
+  const float* post_weight;
+  const float* gate;
+  const float* gamma;
+  const float* beta;  // forward only
+  void* h;            // written by the forward pass, read by the backward pass
+  void* out;          // forward only
+  int64_t batch, seqlen, d_model, mod_rows;
+  float eps;
+  int rms;
+  int io_dtype;
+};
+
+struct AdalnGrads {
+  const void* dout;
+  const void* dres;
+  void* dx;
+  void* dbranch;
+  float* dpost_weight;
+  float* dgate;
+  float* dgamma;
+  float* dbeta;
+};
+
+hipError_t launch_adaln_fwd(const AdalnArgs& a, hipStream_t stream);
+hipError_t launch_adaln_bwd(const AdalnArgs& a, const AdalnGrads& g, void* workspace, hipStream_t stream);
+
+}  // namespace adaln
+
 namespace conv {
 
 // Short causal / anti-causal depthwise convolution (width 4) with optional SiLU.
@@ -84,6 +119,26 @@ struct ConvArgs {
   void* out_r;           // null = reverse direction not computed
   int act;
 };
+
+// Its backward pass; a null dout_f or dout_r leaves that direction out.
+struct ConvBwdArgs {
+  const void* dout_f;
+  const void* dout_r;
+  const void* u;
+  const float* w_f;
+  const float* b_f;
+  const float* w_r;
+  const float* b_r;
+  void* du;
+  float* dw_f;  // null with their direction
+  float* db_f;  // null = not written
+  float* dw_r;
+  float* db_r;
+  int act;
+};
+
+hipError_t launch_conv_bwd(const ConvBwdArgs& a, const BwdPlan& p, int64_t batch, int64_t L, int64_t C, int io_dtype,
+                           void* workspace, hipStream_t stream);
 
 hipError_t launch_conv(const ConvArgs& a, int64_t batch, int64_t L, int64_t C, int io_dtype, hipStream_t stream);
 

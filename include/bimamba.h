@@ -70,7 +70,8 @@ enum {
   BIMAMBA_FLAG_NO_GATE = 1u,  /* out = y_fwd + y_rev, no SiLU(z) factor (z may be NULL) */
   BIMAMBA_FLAG_FWD_ONLY = 2u, /* keep only the forward direction, eq. (4)            */
   BIMAMBA_FLAG_REV_ONLY = 4u, /* keep only the reverse direction, eq. (5)            */
-  BIMAMBA_FLAG_NO_SILU = 16u  /* short convolution only: return the filter output without SiLU */
+  BIMAMBA_FLAG_NO_SILU = 16u, /* short convolution only: return the filter output without SiLU */
+  BIMAMBA_FLAG_RMS_NORM = 32u /* adaln only: the norm leaves out the mean (RMSNorm instead of LayerNorm) */
 };
 
 /* Library version, (major << 16) | (minor << 8) | patch. */
@@ -356,6 +357,82 @@ int bimamba_conv1d_block(const void* u, const float* w_f, const float* b_f, cons
                          const void* cache_in, void* cache_out, void* out_f, void* out_r, int64_t batch,
                          int64_t block_len, int64_t channels, int64_t d_conv, int io_dtype, uint32_t flags,
                          hipStream_t stream);
+
+/* Bytes of device workspace bimamba_conv1d_bidir_bwd needs for this shape; 0 for
+ * an unsupported shape. */
+size_t bimamba_conv1d_bidir_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t channels);
+
+/* Backward pass of bimamba_conv1d_bidir: from dout_f and dout_r, the gradients
+ * of out_f and out_r ([batch, seqlen, channels], io_dtype), with p the filter's
+ * sum before the SiLU and dp = dout * silu'(p) (dp = dout with NO_SILU):
+ *   du[t,c]   = sum_k w_f[c,k] dp_f[t+3-k,c] + sum_k w_r[c,k] dp_r[t-3+k,c]
+ *   dw_f[c,k] = sum_t dp_f[t,c] u[t-3+k,c],   db_f[c] = sum_t dp_f[t,c]
+ *   dw_r[c,k] = sum_t dp_r[t,c] u[t+3-k,c],   db_r[c] = sum_t dp_r[t,c]
+ * (terms outside the sequence are zero; sums over the batch too).  du: like u; the
+ * others fp32, shaped like their parameters, summed in a fixed order.  dout_f or
+ * dout_r may be NULL to leave that direction out (not both): its parameters are
+ * then not read and its gradients must be NULL.  Otherwise dw_* is required and
+ * db_* may be NULL (not written; also allowed where b_* is NULL).  With tied
+ * weights the caller adds the two directions' gradients.  Supported shapes,
+ * alignment, flags, ownership and asynchrony are as for bimamba_conv1d_bidir;
+ * workspace 256-byte aligned, its contents ignored on entry.  No output may
+ * overlap an input, another output or the workspace. */
+int bimamba_conv1d_bidir_bwd(const void* dout_f, const void* dout_r, const void* u, const float* w_f, const float* b_f,
+                             const float* w_r, const float* b_r, void* du, float* dw_f, float* db_f, float* dw_r,
+                             float* db_r, int64_t batch, int64_t seqlen, int64_t channels, int64_t d_conv,
+                             int io_dtype, uint32_t flags, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream);
+
+/* ---- Norm, gate and residual between two blocks ---------------------------
+ * What stands between the mixer of one block and the next block's projection
+ * (Appendix A.1 eq. (10)-(12): the residual sum around the mixer and the
+ * timestep-modulated norm, AdaLN), with an optional norm on the branch itself:
+ *   m'  = branch * post_weight / sqrt(mean(branch^2) + eps)   (post_weight given; else m' = branch)
+ *   h   = x + gate * m'
+ *   out = gamma * (h - mean(h)) / sqrt(var(h) + eps) + beta    (RMS_NORM: without the mean)
+ * Means and variances run over the d_model values of a row; var is the mean of
+ * the squared deviations.  Rows are independent: one call serves a whole batch,
+ * the active block of block decoding, or a single token.
+ *   x, branch, h, out: [batch, seqlen, d_model], io_dtype.  h and out are rounded
+ *   to nearest even from fp32; out is formed from h before its rounding.
+ *   gate, gamma, beta: [mod_rows, d_model] fp32, mod_rows = batch (one row per
+ *   sequence) or 1 (shared by all); NULL means gate = 1, gamma = 1, beta = 0.
+ *   post_weight: [d_model] fp32 or NULL.
+ *   branch may be NULL (then out is the norm of x): post_weight, gate and h must
+ *   be NULL with it.  Otherwise h is required; it may be x itself (the residual
+ *   stream updated in place), and must not otherwise overlap an input.
+ * Supported: d_model a multiple of 8 and at most 8192, 1 <= batch <= 65535, eps
+ * positive and finite; every pointer 16-byte aligned; flags 0 or
+ * BIMAMBA_FLAG_RMS_NORM.  No workspace. */
+int bimamba_adaln_fwd(const void* x, const void* branch, const float* post_weight, const float* gate,
+                      const float* gamma, const float* beta, void* h, void* out, int64_t batch, int64_t seqlen,
+                      int64_t d_model, int64_t mod_rows, float eps, int io_dtype, uint32_t flags, hipStream_t stream);
+
+/* Bytes of device workspace bimamba_adaln_bwd needs for this shape; 0 for an
+ * unsupported shape. */
+size_t bimamba_adaln_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t d_model);
+
+/* Backward pass of bimamba_adaln_fwd, from dout, the gradient of out, and dres,
+ * the gradient that reaches h along the residual stream (NULL = 0).  h is the
+ * forward call's h (x where there was no branch); the row statistics are taken
+ * again from h and branch.  With xhat the normalised h, e = dout * gamma,
+ * r = 1 / sqrt(var(h) + eps), q = 1 / sqrt(mean(branch^2) + eps), mh = branch * q:
+ *   dh = dres + r (e - mean(e) - xhat mean(e xhat))     (RMS_NORM: without mean(e))
+ *   dx = dh,   dgamma = sum dout xhat,   dbeta = sum dout,   dgate = sum dh m'
+ *   dbranch = q (f - mh mean(f mh)), f = gate dh post_weight,  dpost_weight = sum gate dh mh
+ *             (post_weight NULL: dbranch = gate dh)
+ * dgamma, dbeta, dgate [mod_rows, d_model]: sums over a sequence's rows, or over
+ * all rows where mod_rows is 1; dpost_weight [d_model]: over all rows; fp32, in a
+ * fixed order.  Each of the four may be NULL (not written); dgate must be NULL
+ * without branch and dpost_weight without post_weight.  dx (required) may be dres
+ * itself; dbranch is required with branch and must be NULL without it.  Otherwise
+ * no output may overlap an input, another output or the workspace (256-byte
+ * aligned, contents ignored on entry).  The rest is as for bimamba_adaln_fwd. */
+int bimamba_adaln_bwd(const void* dout, const void* dres, const void* h, const void* branch, const float* post_weight,
+                      const float* gate, const float* gamma, void* dx, void* dbranch, float* dpost_weight,
+                      float* dgate, float* dgamma, float* dbeta, int64_t batch, int64_t seqlen, int64_t d_model,
+                      int64_t mod_rows, float eps, int io_dtype, uint32_t flags, void* workspace,
+                      size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }
