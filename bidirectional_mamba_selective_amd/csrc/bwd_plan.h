@@ -9,7 +9,7 @@
 
 namespace bimamba {
 
-// Wavefronts the chunking aims to give the backward kernels.
+// Wavefronts the chunking aims to give the main backward kernel: two per SIMD of a 256-CU part, all of them resident.
 constexpr int64_t kBwdTargetWaves = 2048;
 
 struct BwdPlan {

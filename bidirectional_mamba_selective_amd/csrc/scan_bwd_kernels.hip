@@ -31,9 +31,9 @@
 //   k_bwd_main     walks each chunk left to right with f and p carried and r, G
 //                  entering each tile from its boundary: every gradient above.
 //   k_bwd_reduce   adds the partial sums in a fixed order (no atomics).
-// dB and dC are sums over the channels, which lie across the lanes: the 16
-// tokens of both are reduced together, each step halving the values per lane
-// (70 operations for 32 values; six per value one by one).
+// dB and dC are sums over the channels, which lie across the lanes: a state's 32
+// terms per lane go through LDS, one row per token, and are added in fp32 by two
+// lanes a row while the next state is under way.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -47,6 +47,7 @@ namespace {
 
 constexpr int SUB = static_cast<int>(kSub);
 constexpr int NM = 16;  // states per channel at most
+constexpr int NS = 8;   // states per wavefront of the summary pass
 constexpr int kRsrcWord3 = 0x00020000;  // gfx9 buffer descriptor, untyped 32-bit data format
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, size_t bytes) {
@@ -76,6 +77,8 @@ __device__ __forceinline__ void st_buf(float v, __amdgpu_buffer_rsrc_t r, uint32
                                        const bf16_t*) {
   __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, static_cast<__bf16>(v)), r, voff, soff, CP);
 }
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // v[k] = row k of this lane's column of a tile; rows past the resource's end read as 0.  The row goes into the VGPR
 // offset: the range check covers that one (an SGPR offset is subtracted from the range, which must not underflow).
@@ -199,18 +202,22 @@ __device__ __forceinline__ void tile_inputs(const Args<T>& a, size_t tile, size_
 }
 
 // ---------------------------------------------------------------------------
-// k_bwd_summary: grid (D / 64, nchunk, batch), one wavefront.  DS: bit 0 = the forward layer (f, G), bit 1 = the
-// reverse layer (r, p).
+// k_bwd_summary: grid (D / 64 * ceil(N / NS), nchunk, batch), one wavefront.  DS: bit 0 = the forward layer (f, G), bit
+// 1 = the reverse layer (r, p).  A wavefront takes NS = 8 of the states: its four chains are in LDS, 1 KiB a state, and
+// with all 16 a CU held 10 wavefronts.  Per tile it forms delta, u and dy once more (a sixth of its work), but the waits
+// of its short state steps are covered by 4 wavefronts per SIMD.
 // ---------------------------------------------------------------------------
 template <typename T, int DS, bool GATE>
 __global__ __launch_bounds__(64, 4) void k_bwd_summary(Args<T> a) {
-  __shared__ float sF[(DS & 1) ? NM : 1][64];  // f of the chunk so far, decayed to the chunk end
-  __shared__ float sG[(DS & 1) ? NM : 1][64];  // running G
-  __shared__ float sP[(DS & 2) ? NM : 1][64];
-  __shared__ float sR[(DS & 2) ? NM : 1][64];
+  __shared__ float sF[(DS & 1) ? NS : 1][64];  // f of the chunk so far, decayed to the chunk end
+  __shared__ float sG[(DS & 1) ? NS : 1][64];  // running G
+  __shared__ float sP[(DS & 2) ? NS : 1][64];
+  __shared__ float sR[(DS & 2) ? NS : 1][64];
   const int lane = threadIdx.x;
   const int D = a.Dn, N = a.N;
-  const size_t col0 = static_cast<size_t>(blockIdx.x) * 64;
+  const size_t col0 = static_cast<size_t>(blockIdx.x % (D / 64)) * 64;
+  const int n0 = static_cast<int>(blockIdx.x / (D / 64)) * NS;  // this wavefront's states are n0 + s
+  const int ns = min(NS, N - n0);
   const int c = blockIdx.y;
   const size_t b = blockIdx.z;
   const int t0 = c * a.chunk;
@@ -224,7 +231,7 @@ __global__ __launch_bounds__(64, 4) void k_bwd_summary(Args<T> a) {
   const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.A2T + col0, state_bytes);
   const uint32_t voff4 = static_cast<uint32_t>(lane) * 4u;
   const uint32_t nstride = static_cast<uint32_t>(D) * 4u;
-  for (int n = 0; n < N; ++n) {
+  for (int n = 0; n < ns; ++n) {
     if (DS & 1) sF[n][lane] = sG[n][lane] = 0.0f;
     if (DS & 2) sP[n][lane] = sR[n][lane] = 0.0f;
   }
@@ -245,12 +252,12 @@ __global__ __launch_bounds__(64, 4) void k_bwd_summary(Args<T> a) {
     const size_t keep = j > 0 ? state_bytes : 0;
     const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.Rr + prev * N * D + col0, (DS & 2) ? keep : 0);
     const __amdgpu_buffer_rsrc_t wg = make_rsrc(a.Rg + prev * N * D + col0, (DS & 1) ? keep : 0);
-    float a2_next = ld_buf(ra, voff4, 0, a.A2T);
+    float a2_next = ld_buf(ra, voff4, static_cast<uint32_t>(n0) * nstride, a.A2T);
 #pragma unroll 1
-    for (int n = 0; n < N; ++n) {
+    for (int n = 0; n < ns; ++n) {
       const float a2 = a2_next;
-      a2_next = ld_buf(ra, voff4, static_cast<uint32_t>(min(n + 1, N - 1)) * nstride, a.A2T);
-      const sfloat* bn = scalar_ptr(bt + static_cast<size_t>(n) * 2 * SUB);
+      a2_next = ld_buf(ra, voff4, static_cast<uint32_t>(n0 + min(n + 1, ns - 1)) * nstride, a.A2T);
+      const sfloat* bn = scalar_ptr(bt + static_cast<size_t>(n0 + n) * 2 * SUB);
       float av[SUB], bb[SUB];
 #pragma unroll
       for (int k = 0; k < SUB; ++k) {
@@ -273,7 +280,7 @@ __global__ __launch_bounds__(64, 4) void k_bwd_summary(Args<T> a) {
         }
       }
       const float dec = fast_exp2(a2 * sigma);
-      const uint32_t off = voff4 + static_cast<uint32_t>(n) * nstride;
+      const uint32_t off = voff4 + static_cast<uint32_t>(n0 + n) * nstride;
       if (DS & 1) {
         sF[(DS & 1) ? n : 0][lane] = fmaf(dec, f, sF[(DS & 1) ? n : 0][lane]);
         sG[(DS & 1) ? n : 0][lane] = g;
@@ -286,10 +293,10 @@ __global__ __launch_bounds__(64, 4) void k_bwd_summary(Args<T> a) {
       }
     }
     sigma += tile_sum;
-    if (j > 0) a.sig[prev * D + col0 + lane] = sigma;
+    if (j > 0 && n0 == 0) a.sig[prev * D + col0 + lane] = sigma;
   }
-  for (int n = 0; n < N; ++n) {
-    const size_t o = (cbase * N + n) * D + col0 + lane;
+  for (int n = 0; n < ns; ++n) {
+    const size_t o = (cbase * N + n0 + n) * D + col0 + lane;
     if (DS & 1) {
       a.Sf[o] = sF[(DS & 1) ? n : 0][lane];
       a.Sg[o] = sG[(DS & 1) ? n : 0][lane];
@@ -298,7 +305,7 @@ __global__ __launch_bounds__(64, 4) void k_bwd_summary(Args<T> a) {
       a.Sp[o] = sP[(DS & 2) ? n : 0][lane];
       a.Sr[o] = sR[(DS & 2) ? n : 0][lane];
     }
-    a.P[o] = fast_exp2(a.A2T[static_cast<size_t>(n) * D + col0 + lane] * sigma);
+    a.P[o] = fast_exp2(a.A2T[static_cast<size_t>(n0 + n) * D + col0 + lane] * sigma);
   }
 }
 
@@ -354,32 +361,25 @@ __device__ __forceinline__ float add_dpp(float v) {
   return v + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xf, 0xf, true));
 }
 
-// Sum over the 64 lanes of 32 values at once: every step adds two lane groups and packs two values into one
-// register, so lane l ends with the total of value l / 2.
-__device__ __forceinline__ float lane_sums(float (&v)[2 * SUB], int lane) {
+// Sum over the 64 lanes of 2 SUB = 32 rows of LDS values: lane l adds half l % 2 of row l / 2, 16 bytes at a time, its
+// first chunk turned by the row so that any 16 lanes in a row read 16 different groups of banks.
+struct RowParts {
+  f32x4 q[8];
+};
+
+__device__ __forceinline__ RowParts read_rows(const float (*rows)[64], int lane) {
+  static_assert(SUB == 16, "two lanes a row");
+  const int j = lane >> 1;
+  const f32x4* row = reinterpret_cast<const f32x4*>(&rows[j][(lane & 1) * 32]);
+  RowParts p;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[i + 16]), false, false);
-    v[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[i + 8]), false, false);
-    v[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-  }
-  const bool b3 = (lane & 8) != 0, b2 = (lane & 4) != 0, b1 = (lane & 2) != 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float lo = add_dpp<0x128>(v[i]), hi = add_dpp<0x128>(v[i + 4]);  // row_ror:8
-    v[i] = b3 ? hi : lo;
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float lo = add_dpp<0x141>(v[i]), hi = add_dpp<0x141>(v[i + 2]);  // row_half_mirror
-    v[i] = b2 ? hi : lo;
-  }
-  const float lo = add_dpp<0x4E>(v[0]), hi = add_dpp<0x4E>(v[1]);  // quad_perm [2,3,0,1]
-  return add_dpp<0xB1>(b1 ? hi : lo);                              // quad_perm [1,0,3,2]
+  for (int i = 0; i < 8; ++i) p.q[i] = row[(i + j) & 7];
+  return p;
+}
+
+__device__ __forceinline__ float total(const RowParts& p) {
+  const f32x4 s = ((p.q[0] + p.q[1]) + (p.q[2] + p.q[3])) + ((p.q[4] + p.q[5]) + (p.q[6] + p.q[7]));
+  return add_dpp<0xB1>((s[0] + s[1]) + (s[2] + s[3]));  // quad_perm [1,0,3,2]: the row's other half
 }
 
 // ---------------------------------------------------------------------------
@@ -390,6 +390,7 @@ __global__ __launch_bounds__(64, 2) void k_bwd_main(Args<T> a) {
   __shared__ float sF[(DS & 1) ? NM : 1][64];
   __shared__ float sP[(DS & 2) ? NM : 1][64];
   __shared__ float sA[NM][64];  // dA of the chunk so far
+  __shared__ __align__(16) float sV[2 * SUB][64];  // a state's terms of dB and dC, one row per token
   const int lane = threadIdx.x;
   const int D = a.Dn, N = a.N;
   const size_t col0 = static_cast<size_t>(blockIdx.x) * 64;
@@ -452,6 +453,11 @@ __global__ __launch_bounds__(64, 2) void k_bwd_main(Args<T> a) {
       const uint32_t s1 = static_cast<uint32_t>(min(n + 1, N - 1)) * nstride;
       a2_next = ld_buf(ra, voff4, s1, a.A2T);
       const sfloat* bn = scalar_ptr(bt + static_cast<size_t>(n) * 2 * SUB);
+      // the previous state's terms: read here, added after the right-to-left walk, so that their way through LDS costs
+      // no wait (state 0 reads what the tile before left and drops it)
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      const RowParts parts = read_rows(sV, lane);
+      __builtin_amdgcn_sched_barrier(0);
       // the chunk end's resource is empty: the boundary state reads as 0 and the decay is 1
       const float q = fast_exp2(a2 * sj);
       float r = 0.0f, g = 0.0f;
@@ -465,23 +471,31 @@ __global__ __launch_bounds__(64, 2) void k_bwd_main(Args<T> a) {
         gj_next = ld_buf<kStream>(rg, voff4 + s1, 0, a.Rg);
         cg_next = ld_buf(rcg, voff4, s1, a.Sg);
       }
-      float av[SUB];
+      float av[SUB], bb[SUB];
 #pragma unroll
-      for (int k = 0; k < SUB; ++k) av[k] = fast_exp2(dl[k] * a2);
-      // right to left: r before each token (for w) and after it, gf
-      float rv[SUB + 1], v[2 * SUB];
+      for (int k = 0; k < SUB; ++k) {
+        av[k] = fast_exp2(dl[k] * a2);
+        bb[k] = u[k] * bn[k];
+      }
+      // right to left: r before each token (for w) and after it, gf, G
+      float rv[SUB + 1], gf[SUB];
       rv[SUB] = r;
 #pragma unroll
       for (int k = SUB - 1; k >= 0; --k) {
         if (DS & 2) {
-          r = fmaf(av[k], r, u[k] * bn[k]);
+          r = fmaf(av[k], r, bb[k]);
           rv[k] = r;
         }
         if (DS & 1) {
-          const float gf = fmaf(bn[SUB + k], dy[k], g);
-          v[k] = gf;
-          g = av[k] * gf;
+          gf[k] = fmaf(bn[SUB + k], dy[k], g);
+          g = av[k] * gf[k];
         }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      {
+        const float s = total(parts);
+        if (n > 0 && (lane & 1) == 0) pbc[(n - 1) * 2 * SUB + (lane >> 1)] = s;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       }
       // left to right: f and p, and everything formed from the four states of a token
       float f = (DS & 1) ? sF[(DS & 1) ? n : 0][lane] : 0.0f;
@@ -491,9 +505,9 @@ __global__ __launch_bounds__(64, 2) void k_bwd_main(Args<T> a) {
       for (int k = 0; k < SUB; ++k) {
         float w, gs, hs;
         if (DS & 1) {
-          w = (av[k] * v[k]) * f;
-          gs = v[k];
-          f = fmaf(av[k], f, u[k] * bn[k]);
+          w = (av[k] * gf[k]) * f;
+          gs = gf[k];
+          f = fmaf(av[k], f, bb[k]);
           hs = f;
         }
         if (DS & 2) {
@@ -507,15 +521,17 @@ __global__ __launch_bounds__(64, 2) void k_bwd_main(Args<T> a) {
         dA = fmaf(dl[k], w, dA);
         du[k] = fmaf(bn[k], gs, du[k]);
         if (GATE) y[k] = fmaf(bn[SUB + k], hs, y[k]);
-        v[k] = u[k] * gs;
-        v[SUB + k] = dy[k] * hs;
+        sV[k][lane] = u[k] * gs;
+        sV[SUB + k][lane] = dy[k] * hs;
       }
       if (DS & 1) sF[(DS & 1) ? n : 0][lane] = f;
       if (DS & 2) sP[(DS & 2) ? n : 0][lane] = p;
       sA[n][lane] = dA;
-      const float s = lane_sums(v, lane);
-      if ((lane & 1) == 0) pbc[n * 2 * SUB + (lane >> 1)] = s;
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const float last = total(read_rows(sV, lane));
+    if ((lane & 1) == 0) pbc[(N - 1) * 2 * SUB + (lane >> 1)] = last;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     // the gradients of the token's own inputs
     float xr[SUB], dr[SUB];
     load_col(a.x + tile, bytes, voff, row_bytes, xr);
@@ -532,6 +548,7 @@ __global__ __launch_bounds__(64, 2) void k_bwd_main(Args<T> a) {
     }
     store_col(dr, a.ddt + tile, bytes, voff, row_bytes);
     store_col(du, a.dx + tile, bytes, voff, row_bytes);
+    __builtin_amdgcn_sched_barrier(0);
     if (GATE) {
       float zr[SUB], gr[SUB];
       load_col(a.z + tile, bytes, voff, row_bytes, zr);
@@ -575,7 +592,7 @@ __global__ __launch_bounds__(256) void k_bwd_reduce(const float* __restrict__ pb
     for (int w = 0; w < W; ++w) s += src[static_cast<size_t>(w) * per];
     const int n = static_cast<int>(i / (2 * SUB)), k = static_cast<int>(i % (2 * SUB));
     const size_t b = gt / ntile;
-    const int t = static_cast<int>(gt % ntile) * SUB + (k & (SUB - 1));
+    const int t = static_cast<int>(gt % ntile) * SUB + k % SUB;
     if (t < L) st_elem(s, (k < SUB ? dB : dC) + (b * L + t) * N + n);
     return;
   }
@@ -601,7 +618,8 @@ __global__ __launch_bounds__(256) void k_bwd_reduce(const float* __restrict__ pb
 template <typename T, int DS, bool GATE>
 hipError_t launch_passes(const Args<T>& a, const BwdPlan& p, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(a.Dn / 64), static_cast<unsigned>(a.nchunk), static_cast<unsigned>(p.batch));
-  hipLaunchKernelGGL((k_bwd_summary<T, DS, GATE>), grid, dim3(64), 0, stream, a);
+  const dim3 sgrid(grid.x * static_cast<unsigned>((a.N + NS - 1) / NS), grid.y, grid.z);
+  hipLaunchKernelGGL((k_bwd_summary<T, DS, GATE>), sgrid, dim3(64), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const size_t nth = static_cast<size_t>(p.batch) * a.N * a.Dn;
