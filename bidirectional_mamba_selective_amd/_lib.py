@@ -153,14 +153,22 @@ def bimamba_scan_block_workspace_bytes(batch: int, block_len: int, d_inner: int,
     return int(load().bimamba_scan_block_workspace_bytes(batch, block_len, d_inner, d_state))
 
 
-def _torch():
-    import torch
+_torch_module = None
+_raw_stream = None  # the current stream's handle without a Stream object around it (2 us a call), where torch has it
 
-    return torch
+
+def _torch():
+    global _torch_module, _raw_stream
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return _torch_module
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()  # the declared argument types make it a void pointer
 
 
 def _bytes_of(t):
@@ -191,6 +199,8 @@ def _io_dtype(x):
 def _check(t, name, shape, dtype, device):
     if t is None:
         return
+    if t.is_cuda and t.device == device and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        return  # what nearly every call passes; below, what is wrong with the others
     if not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be on {device}")
     if t.dtype != dtype:
@@ -225,8 +235,11 @@ def _common(x, dt, A, B, C, D, z, dt_bias, out):
 
 def _stream(stream, device):
     torch = _torch()
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _on(stream):
@@ -237,6 +250,42 @@ def _on(stream):
 
     torch = _torch()
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+class _Here:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+class _There:
+    """The device (and, where given, the stream) of a call as the current one."""
+
+    def __init__(self, device, stream):
+        torch = _torch()
+        self._parts = [torch.cuda.device(device)] + ([] if stream is None else [torch.cuda.stream(stream)])
+
+    def __enter__(self):
+        for p in self._parts:
+            p.__enter__()
+
+    def __exit__(self, *exc):
+        for p in reversed(self._parts):
+            p.__exit__(*exc)
+        return False
+
+
+def _at(device, stream):
+    """Context of a whole call: its launches go to the tensors' device whatever the current one is, and what the
+    binding allocates is allocated on the stream that the kernels run on (see _on)."""
+    if stream is None and device.type == "cuda" and device.index == _torch().cuda.current_device():
+        return _HERE
+    return _There(device, stream)
 
 
 def bimamba_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, out=None, flags: int = 0, workspace=None,
@@ -338,23 +387,31 @@ def bimamba_scan_bwd_workspace_bytes(batch: int, seqlen: int, d_inner: int, d_st
     return int(load().bimamba_scan_bwd_workspace_bytes(batch, seqlen, d_inner, d_state))
 
 
-def _grads(grads, shapes, device):
-    """The gradient tensors of a backward call: the caller's (grads, checked) or new ones.  shapes: name ->
-    (shape, dtype), or None for a gradient that the call does not have."""
-    torch = _torch()
-    got = {}
-    grads = grads or {}
-    unknown = [k for k, v in grads.items() if v is not None and shapes.get(k) is None]
+def _grads(grads, like):
+    """The gradient tensors of a backward call: the caller's (grads, checked) or new ones.  like: name -> the input
+    whose shape and type the gradient has, or None for a gradient that the call does not have."""
+    empty_like = _torch().empty_like
+    if not grads:
+        return {k: None if t is None else empty_like(t) for k, t in like.items()}
+    unknown = [k for k, v in grads.items() if v is not None and like.get(k) is None]
     if unknown:
         raise ValueError(f"no gradient of {', '.join(sorted(unknown))} in this call")
-    for k, s in shapes.items():
-        t = grads.get(k)
-        if s is not None and t is None:
-            t = torch.empty(s[0], dtype=s[1], device=device)
-        elif s is not None:
-            _check(t, f"grads[{k!r}]", s[0], s[1], device)
-        got[k] = t
+    got = {}
+    for k, t in like.items():
+        g = grads.get(k)
+        if t is not None and g is None:
+            g = empty_like(t)
+        elif t is not None:
+            _check(g, f"grads[{k!r}]", t.shape, t.dtype, t.device)
+        got[k] = g
     return got
+
+
+def _workspace(workspace, need, device):
+    """(tensor, bytes) of the caller's workspace, checked, or of a new one."""
+    if workspace is not None:
+        return workspace, _nbytes(workspace, device)
+    return _torch().empty(max(need, 1), dtype=_torch().uint8, device=device), need
 
 
 def bimamba_scan_bwd(dout, x, dt, A, B, C, D=None, z=None, dt_bias=None, flags: int = 0, grads=None, workspace=None,
@@ -364,24 +421,20 @@ def bimamba_scan_bwd(dout, x, dt, A, B, C, D=None, z=None, dt_bias=None, flags: 
     inputs, None for an optional input that was not given.  grads may hold tensors to write into."""
     torch = _torch()
     lib = load()
-    if x.dim() != 3:
-        raise ValueError("x must be [batch, seqlen, d_inner]")
-    with torch.cuda.device(x.device), _on(stream):
-        nb, L, nd, ns, dout = _common(x, dt, A, B, C, D, z, dt_bias, dout)
-        gated = not flags & FLAG_NO_GATE
-        f32 = torch.float32
-        g = _grads(grads, {"x": (x.shape, x.dtype), "dt": (x.shape, x.dtype), "A": (A.shape, f32),
-                           "B": (B.shape, x.dtype), "C": (C.shape, x.dtype),
-                           "D": ((nd,), f32) if D is not None else None, "z": (x.shape, x.dtype) if gated else None,
-                           "dt_bias": ((nd,), f32) if dt_bias is not None else None}, x.device)
-        if workspace is None:
-            need = int(lib.bimamba_scan_bwd_workspace_bytes(nb, L, nd, ns))
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
+    if x.dim() != 3 or dout is None:
+        raise ValueError("x and dout must be [batch, seqlen, d_inner]")
+    dev = x.device
+    with _at(dev, stream):
+        _check(dout, "dout", x.shape, x.dtype, dev)
+        nb, L, nd, ns, _ = _common(x, dt, A, B, C, D, z, dt_bias, dout)
+        g = _grads(grads, {"x": x, "dt": dt, "A": A, "B": B, "C": C, "D": D,
+                           "z": None if flags & FLAG_NO_GATE else z, "dt_bias": dt_bias})
+        workspace, wbytes = _workspace(workspace, lib.bimamba_scan_bwd_workspace_bytes(nb, L, nd, ns), dev)
         st = lib.bimamba_scan_bwd(_ptr(dout), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
                                   _ptr(dt_bias), _ptr(g["x"]), _ptr(g["dt"]), _ptr(g["A"]), _ptr(g["B"]),
                                   _ptr(g["C"]), _ptr(g["D"]), _ptr(g["z"]), _ptr(g["dt_bias"]), nb, L, nd, ns,
-                                  _io_dtype(x), flags, _ptr(workspace), _nbytes(workspace, x.device),
-                                  _stream(stream, x.device))
+                                  _io_dtype(x), flags, _ptr(workspace), wbytes,
+                                  _stream(stream, dev))
     if st != BIMAMBA_OK:
         raise BimambaError(st, "bimamba_scan_bwd")
     return g
@@ -605,20 +658,17 @@ def bimamba_conv1d_bidir_bwd(dout_f, dout_r, u, w_f=None, b_f=None, w_r=None, b_
             raise ValueError(f"dout_{name} and w_{name} come together")
         if d is None and b is not None:
             raise ValueError(f"b_{name} without dout_{name}")
-    with torch.cuda.device(u.device), _on(stream):
-        # the gradients of the outputs have the outputs' shapes
+    dev = u.device
+    with _at(dev, stream):
+        _check(dout_f, "dout_f", u.shape, u.dtype, dev)
+        _check(dout_r, "dout_r", u.shape, u.dtype, dev)
         nb, L, nc, K, dout_f, dout_r = _conv_common(u, w_f, b_f, w_r, b_r, dout_f, dout_r)
-        f32 = torch.float32
-        g = _grads(grads, {"u": (u.shape, u.dtype), **{k: None if t is None else (t.shape, f32) for k, t in
-                                                        (("w_f", w_f), ("b_f", b_f), ("w_r", w_r), ("b_r", b_r))}},
-                   u.device)
-        if workspace is None:
-            need = int(lib.bimamba_conv1d_bidir_bwd_workspace_bytes(nb, L, nc))
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=u.device)
+        g = _grads(grads, {"u": u, "w_f": w_f, "b_f": b_f, "w_r": w_r, "b_r": b_r})
+        workspace, wbytes = _workspace(workspace, lib.bimamba_conv1d_bidir_bwd_workspace_bytes(nb, L, nc), dev)
         st = lib.bimamba_conv1d_bidir_bwd(_ptr(dout_f), _ptr(dout_r), _ptr(u), _ptr(w_f), _ptr(b_f), _ptr(w_r),
                                           _ptr(b_r), _ptr(g["u"]), _ptr(g["w_f"]), _ptr(g["b_f"]), _ptr(g["w_r"]),
                                           _ptr(g["b_r"]), nb, L, nc, K, _io_dtype(u), flags, _ptr(workspace),
-                                          _nbytes(workspace, u.device), _stream(stream, u.device))
+                                          wbytes, _stream(stream, dev))
     if st != BIMAMBA_OK:
         raise BimambaError(st, "bimamba_conv1d_bidir_bwd")
     return g
@@ -648,7 +698,8 @@ def bimamba_adaln_fwd(x, gamma=None, beta=None, branch=None, post_weight=None, g
     branch h is x.  h may be given as x to update the residual stream in place."""
     torch = _torch()
     lib = load()
-    with torch.cuda.device(x.device), _on(stream):
+    dev = x.device
+    with _at(dev, stream):
         nb, L, nd, rows = _adaln_common(x, "x", gamma, beta, branch, post_weight, gate)
         if branch is not None and h is None:
             h = torch.empty_like(x)
@@ -658,7 +709,7 @@ def bimamba_adaln_fwd(x, gamma=None, beta=None, branch=None, post_weight=None, g
         _check(out, "out", x.shape, x.dtype, x.device)
         st = lib.bimamba_adaln_fwd(_ptr(x), _ptr(branch), _ptr(post_weight), _ptr(gate), _ptr(gamma), _ptr(beta),
                                    _ptr(h), _ptr(out), nb, L, nd, rows, eps, _io_dtype(x), flags,
-                                   _stream(stream, x.device))
+                                   _stream(stream, dev))
     if st != BIMAMBA_OK:
         raise BimambaError(st, "bimamba_adaln_fwd")
     return (x if branch is None else h), out
@@ -675,23 +726,19 @@ def bimamba_adaln_bwd(dout, dres, h, gamma=None, beta=None, branch=None, post_we
     that was not given.  grads may hold tensors to write into; grads["x"] may be dres."""
     torch = _torch()
     lib = load()
-    with torch.cuda.device(h.device), _on(stream):
+    dev = h.device
+    with _at(dev, stream):
         nb, L, nd, rows = _adaln_common(h, "h", gamma, beta, branch, post_weight, gate)
         _check(dout, "dout", h.shape, h.dtype, h.device)
         _check(dres, "dres", h.shape, h.dtype, h.device)
-        f32 = torch.float32
-        g = _grads(grads, {"x": (h.shape, h.dtype), "branch": None if branch is None else (h.shape, h.dtype),
-                           **{k: None if t is None else (t.shape, f32) for k, t in
-                              (("gamma", gamma), ("beta", beta), ("post_weight", post_weight), ("gate", gate))}},
-                   h.device)
-        if workspace is None:
-            need = int(lib.bimamba_adaln_bwd_workspace_bytes(nb, L, nd))
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=h.device)
+        g = _grads(grads, {"x": h, "gamma": gamma, "beta": beta, "branch": branch, "post_weight": post_weight,
+                           "gate": gate})
+        workspace, wbytes = _workspace(workspace, lib.bimamba_adaln_bwd_workspace_bytes(nb, L, nd), dev)
         st = lib.bimamba_adaln_bwd(_ptr(dout), _ptr(dres), _ptr(h), _ptr(branch), _ptr(post_weight), _ptr(gate),
                                    _ptr(gamma), _ptr(g["x"]), _ptr(g["branch"]), _ptr(g["post_weight"]),
                                    _ptr(g["gate"]), _ptr(g["gamma"]), _ptr(g["beta"]), nb, L, nd, rows, eps,
-                                   _io_dtype(h), flags, _ptr(workspace), _nbytes(workspace, h.device),
-                                   _stream(stream, h.device))
+                                   _io_dtype(h), flags, _ptr(workspace), wbytes,
+                                   _stream(stream, dev))
     if st != BIMAMBA_OK:
         raise BimambaError(st, "bimamba_adaln_bwd")
     return g

@@ -405,10 +405,10 @@ struct ReduceArgs {
   int mod_rows_one;   // dst[0..2] are one row for the whole batch
 };
 
-// 64 columns of one sum and one output row per workgroup; its 4 wavefronts take every fourth partial sum and meet in
+// 64 columns of one sum and one output row per workgroup; its 16 wavefronts take every sixteenth partial sum and meet in
 // LDS.
-__global__ __launch_bounds__(256) void k_adaln_reduce(ReduceArgs a) {
-  __shared__ float s[4][64];
+__global__ __launch_bounds__(1024) void k_adaln_reduce(ReduceArgs a) {
+  __shared__ float s[16][64];
   const int which = blockIdx.z;
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const bool whole = which == 3 || a.mod_rows_one;  // one row, summed over the batch
@@ -420,12 +420,14 @@ __global__ __launch_bounds__(256) void k_adaln_reduce(ReduceArgs a) {
   if (col < a.d) {
     const float* p = a.part + (first * kSums + which) * a.d + col;
 #pragma unroll 8
-    for (int64_t i = wv; i < n; i += 4) t += p[i * kSums * a.d];
+    for (int64_t i = wv; i < n; i += 16) t += p[i * kSums * a.d];
   }
   s[wv][lane] = t;
   __syncthreads();
-  if (wv == 0 && col < a.d)
-    a.dst[which][(whole ? 0 : blockIdx.y) * a.d + col] = (s[0][lane] + s[1][lane]) + (s[2][lane] + s[3][lane]);
+  if (wv != 0 || col >= a.d) return;
+#pragma unroll
+  for (int w = 1; w < 16; ++w) t += s[w][lane];
+  a.dst[which][(whole ? 0 : blockIdx.y) * a.d + col] = t;
 }
 
 template <typename F>
@@ -470,7 +472,7 @@ hipError_t bwd_typed(const AdalnArgs& in, const AdalnGrads& g, const Plan& p, vo
                      p.chunks * row_groups(p.waves), in.batch, in.mod_rows == 1};
   hipLaunchKernelGGL(k_adaln_reduce, dim3(static_cast<unsigned>((in.d_model + 63) / 64),
                                           static_cast<unsigned>(in.mod_rows == 1 ? 1 : in.batch), kSums),
-                     dim3(256), 0, stream, r);
+                     dim3(1024), 0, stream, r);
   return hipGetLastError();
 }
 
@@ -482,7 +484,7 @@ hipError_t launch_adaln_fwd(const AdalnArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_adaln_bwd(const AdalnArgs& a, const AdalnGrads& g, void* workspace, hipStream_t stream) {
-  const Plan p = make_plan(a.batch, a.seqlen, a.d_model, kBwdGroups);
+  const Plan p = make_plan(a.batch, a.seqlen, a.d_model, bwd_groups(waves_for(a.d_model)));
   return a.io_dtype == 1 ? bwd_typed<bf16_t>(a, g, p, workspace, stream)
                          : bwd_typed<float>(a, g, p, workspace, stream);
 }

@@ -14,7 +14,6 @@ namespace adaln {
 constexpr int64_t kVec = 8;           // values per thread and vector load
 constexpr int64_t kMaxWidth = 8192;   // widest row: 16 wavefronts, one vector per lane
 constexpr int64_t kFwdGroups = 2048;  // workgroups the forward pass aims at (8 per CU)
-constexpr int64_t kBwdGroups = 1024;  // the backward pass: 4 per CU (its partial sums grow with them)
 constexpr int kSums = 4;              // column sums of the backward pass: dgamma, dbeta, dgate, dpost_weight
 
 // Wavefronts per row, one vector per lane.  A row of up to 512 values stays in one wavefront, and its sums need no
@@ -23,6 +22,14 @@ inline int waves_for(int64_t d) {
   int w = 1;
   while (w * 64 * kVec < d) w *= 2;
   return w;
+}
+
+// Workgroups the backward pass aims at: as many as 256 CUs hold at once (its 132 to 157 registers allow 3 wavefronts per
+// SIMD, so 12 per CU), in one round: 8 x 8192 rows of 2048 in 320 + 11 us (kernel and partial sums) at 768, 373 + 15 us
+// at 1024 (a third of a round is left over), 335 + 8 us at 512.
+inline int64_t bwd_groups(int waves) {
+  const int per_wg = waves == 1 ? 4 : waves;
+  return 256 * (per_wg >= 8 ? 1 : 12 / per_wg);
 }
 
 // Rows a workgroup holds at once.

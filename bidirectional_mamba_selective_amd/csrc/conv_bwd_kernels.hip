@@ -286,9 +286,9 @@ struct BwdReduceArgs {
   int64_t C, rows;
 };
 
-// 64 channels of one sum per workgroup; 4 wavefronts take every fourth partial sum and meet in LDS.
-__global__ __launch_bounds__(256) void k_conv_bwd_reduce(BwdReduceArgs a) {
-  __shared__ float red[4][64];
+// 64 channels of one sum per workgroup; 16 wavefronts take every sixteenth partial sum and meet in LDS.
+__global__ __launch_bounds__(1024) void k_conv_bwd_reduce(BwdReduceArgs a) {
+  __shared__ float red[16][64];
   const int s = blockIdx.y, k = s % 5;
   float* dst = s < 5 ? (k < 4 ? a.dw_f : a.db_f) : (k < 4 ? a.dw_r : a.db_r);
   if (!dst) return;
@@ -298,12 +298,13 @@ __global__ __launch_bounds__(256) void k_conv_bwd_reduce(BwdReduceArgs a) {
   if (c < a.C) {
     const float* p = a.part + s * a.C + c;
 #pragma unroll 8
-    for (int64_t i = wv; i < a.rows; i += 4) t += p[i * kBwdSums * a.C];
+    for (int64_t i = wv; i < a.rows; i += 16) t += p[i * kBwdSums * a.C];
   }
   red[wv][lane] = t;
   __syncthreads();
   if (wv != 0 || c >= a.C) return;
-  t = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+#pragma unroll
+  for (int w = 1; w < 16; ++w) t += red[w][lane];
   if (k < 4) dst[c * 4 + k] = t;
   else dst[c] = t;
 }
@@ -321,7 +322,7 @@ hipError_t launch_typed(const ConvBwdArgs& in, const BwdPlan& p, int64_t batch, 
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const BwdReduceArgs r{static_cast<const float*>(ws), in.dw_f, in.db_f, in.dw_r, in.db_r, C, batch * p.groups};
-  hipLaunchKernelGGL(k_conv_bwd_reduce, dim3(static_cast<unsigned>((C + 63) / 64), kBwdSums), dim3(256), 0, stream, r);
+  hipLaunchKernelGGL(k_conv_bwd_reduce, dim3(static_cast<unsigned>((C + 63) / 64), kBwdSums), dim3(1024), 0, stream, r);
   return hipGetLastError();
 }
 
