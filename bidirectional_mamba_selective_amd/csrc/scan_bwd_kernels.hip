@@ -34,6 +34,16 @@
 // dB and dC are sums over the channels, which lie across the lanes: a state's 32
 // terms per lane go through LDS, one row per token, and are added in fp32 by two
 // lanes a row while the next state is under way.
+//
+// What bounds it, at 8192 tokens x 4096 channels x 16 states, bf16, both directions (0.71 ms a call; its tensors alone
+// would stream in 0.09 ms): vector issue.  k_bwd_main, 490 us, runs 28 operations per (token, channel, state) and
+// k_bwd_summary, 248 us, 12; at the 2.3 clocks that independent operations take that is 0.4 ms.  The rest: scalar
+// operands back to back (3.5 clocks), exponentials (7), and the loads at a tile's two ends, which two wavefronts per SIMD
+// do not cover.  Measured and not kept for k_bwd_main: tiles of 12 tokens at 3 wavefronts per SIMD 552 us and of 8 at 4
+// 671 (a tile's boundary states are read and written that much more often); lane swaps and DPP adds for the sums over
+// channels 550; the same sums on the matrix cores, exact in 4 x 4 blocks, 603; the next tile brought to LDS or to
+// registers during the current one 586 and 490; B and C loaded a state ahead into a second set of SGPRs 518.
+// k_bwd_carry 15 us, k_bwd_reduce 14 us and k_bwd_stage 5 us are streams of the workspace.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -204,8 +214,8 @@ __device__ __forceinline__ void tile_inputs(const Args<T>& a, size_t tile, size_
 // ---------------------------------------------------------------------------
 // k_bwd_summary: grid (D / 64 * ceil(N / NS), nchunk, batch), one wavefront.  DS: bit 0 = the forward layer (f, G), bit
 // 1 = the reverse layer (r, p).  A wavefront takes NS = 8 of the states: its four chains are in LDS, 1 KiB a state, and
-// with all 16 a CU held 10 wavefronts.  Per tile it forms delta, u and dy once more (a sixth of its work), but the waits
-// of its short state steps are covered by 4 wavefronts per SIMD.
+// with all 16 a CU held 10 wavefronts and took 312 us instead of 248 (6 and 4 states: 293, 283).  Per tile it forms
+// delta, u and dy once more, but the waits of its short state steps are covered by 4 wavefronts per SIMD.
 // ---------------------------------------------------------------------------
 template <typename T, int DS, bool GATE>
 __global__ __launch_bounds__(64, 4) void k_bwd_summary(Args<T> a) {
@@ -361,7 +371,7 @@ __device__ __forceinline__ float add_dpp(float v) {
   return v + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xf, 0xf, true));
 }
 
-// Sum over the 64 lanes of 2 SUB = 32 rows of LDS values: lane l adds half l % 2 of row l / 2, 16 bytes at a time, its
+// Sum over the 64 lanes of 2 SUB = 32 rows of LDS values: lane l takes half l % 2 of row l / 2, 16 bytes at a time, its
 // first chunk turned by the row so that any 16 lanes in a row read 16 different groups of banks.
 struct RowParts {
   f32x4 q[8];
