@@ -653,16 +653,22 @@ def bimamba_conv1d_bidir_bwd(dout_f, dout_r, u, w_f=None, b_f=None, w_r=None, b_
     does not have.  grads may hold tensors to write into."""
     torch = _torch()
     lib = load()
-    for d, w, b, name in ((dout_f, w_f, b_f, "f"), (dout_r, w_r, b_r, "r")):
-        if (d is None) != (w is None):
-            raise ValueError(f"dout_{name} and w_{name} come together")
-        if d is None and b is not None:
-            raise ValueError(f"b_{name} without dout_{name}")
-    dev = u.device
+    if (dout_f is None) != (w_f is None) or (dout_r is None) != (w_r is None):
+        raise ValueError("dout_f comes with w_f and dout_r with w_r")
+    if (dout_f is None and b_f is not None) or (dout_r is None and b_r is not None):
+        raise ValueError("a bias without its direction")
+    if u.dim() != 3 or (w_f is None and w_r is None):
+        raise ValueError("u must be [batch, seqlen, channels], with at least one direction")
+    nb, L, nc = u.shape
+    K = (w_r if w_f is None else w_f).shape[-1]
+    dev, io, f32 = u.device, u.dtype, torch.float32
     with _at(dev, stream):
-        _check(dout_f, "dout_f", u.shape, u.dtype, dev)
-        _check(dout_r, "dout_r", u.shape, u.dtype, dev)
-        nb, L, nc, K, dout_f, dout_r = _conv_common(u, w_f, b_f, w_r, b_r, dout_f, dout_r)
+        _check(u, "u", u.shape, io, dev)
+        for d, w, b, name in ((dout_f, w_f, b_f, "f"), (dout_r, w_r, b_r, "r")):
+            if d is not None:
+                _check(d, "dout_" + name, u.shape, io, dev)
+                _check(w, "w_" + name, (nc, K), f32, dev)
+                _check(b, "b_" + name, (nc,), f32, dev)
         g = _grads(grads, {"u": u, "w_f": w_f, "b_f": b_f, "w_r": w_r, "b_r": b_r})
         workspace, wbytes = _workspace(workspace, lib.bimamba_conv1d_bidir_bwd_workspace_bytes(nb, L, nc), dev)
         st = lib.bimamba_conv1d_bidir_bwd(_ptr(dout_f), _ptr(dout_r), _ptr(u), _ptr(w_f), _ptr(b_f), _ptr(w_r),
@@ -679,15 +685,17 @@ def _adaln_common(x, name, gamma, beta, branch, post_weight, gate):
     if x.dim() != 3:
         raise ValueError(f"{name} must be [batch, seqlen, d_model]")
     nb, L, nd = x.shape
-    mods = [(k, t) for k, t in (("gamma", gamma), ("beta", beta), ("gate", gate)) if t is not None]
-    rows = mods[0][1].shape[0] if mods and mods[0][1].dim() == 2 else nb
-    if rows not in (1, nb):
-        raise ValueError(f"{mods[0][0]} must have one row, or one per sequence")
-    for k, t in mods:
-        _check(t, k, (rows, nd), torch.float32, x.device)
-    _check(x, name, (nb, L, nd), x.dtype, x.device)
-    _check(branch, "branch", (nb, L, nd), x.dtype, x.device)
-    _check(post_weight, "post_weight", (nd,), torch.float32, x.device)
+    dev, f32 = x.device, torch.float32
+    first = gamma if gamma is not None else beta if beta is not None else gate
+    rows = first.shape[0] if first is not None and first.dim() == 2 else nb
+    if rows != 1 and rows != nb:
+        raise ValueError("gamma, beta and gate must have one row, or one per sequence")
+    _check(gamma, "gamma", (rows, nd), f32, dev)
+    _check(beta, "beta", (rows, nd), f32, dev)
+    _check(gate, "gate", (rows, nd), f32, dev)
+    _check(x, name, x.shape, x.dtype, dev)
+    _check(branch, "branch", x.shape, x.dtype, dev)
+    _check(post_weight, "post_weight", (nd,), f32, dev)
     return nb, L, nd, rows
 
 
