@@ -35,15 +35,17 @@
 // terms per lane go through LDS, one row per token, and are added in fp32 by two
 // lanes a row while the next state is under way.
 //
-// What bounds it, at 8192 tokens x 4096 channels x 16 states, bf16, both directions (0.71 ms a call; its tensors alone
-// would stream in 0.09 ms): vector issue.  k_bwd_main, 490 us, runs 28 operations per (token, channel, state) and
-// k_bwd_summary, 248 us, 12; at the 2.3 clocks that independent operations take that is 0.4 ms.  The rest: scalar
+// What bounds it, at 8192 tokens x 4096 channels x 16 states, bf16, both directions (0.67 ms a call; its tensors alone
+// would stream in 0.09 ms): vector issue.  k_bwd_main, 467 us, runs 28 operations per (token, channel, state) and
+// k_bwd_summary, 233 us, 12; at the 2.3 clocks that independent operations take that is 0.4 ms.  The rest: scalar
 // operands back to back (3.5 clocks), exponentials (7), and the loads at a tile's two ends, which two wavefronts per SIMD
 // do not cover.  Measured and not kept for k_bwd_main: tiles of 12 tokens at 3 wavefronts per SIMD 552 us and of 8 at 4
 // 671 (a tile's boundary states are read and written that much more often); lane swaps and DPP adds for the sums over
 // channels 550; the same sums on the matrix cores, exact in 4 x 4 blocks, 603; the next tile brought to LDS or to
 // registers during the current one 586 and 490; B and C loaded a state ahead into a second set of SGPRs 518.
-// k_bwd_carry 15 us, k_bwd_reduce 14 us and k_bwd_stage 5 us are streams of the workspace.
+// The wavefronts of a SIMD take turns: the exponentials (in k_bwd_main the right-to-left walk and a tile's two ends too) run at a raised wave
+// priority, so that one wavefront's slow operations and dependent steps fall into the other's independent ones: 493 ->
+// 467 us, 247 -> 233 us.  k_bwd_carry 15 us, k_bwd_reduce 14 us and k_bwd_stage 5 us are streams of the workspace.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -267,6 +269,7 @@ __global__ __launch_bounds__(64, 4) void k_bwd_summary(Args<T> a) {
     for (int n = 0; n < ns; ++n) {
       const float a2 = a2_next;
       a2_next = ld_buf(ra, voff4, static_cast<uint32_t>(n0 + min(n + 1, ns - 1)) * nstride, a.A2T);
+      __builtin_amdgcn_s_setprio(1);
       const sfloat* bn = scalar_ptr(bt + static_cast<size_t>(n0 + n) * 2 * SUB);
       float av[SUB], bb[SUB];
 #pragma unroll
@@ -274,6 +277,7 @@ __global__ __launch_bounds__(64, 4) void k_bwd_summary(Args<T> a) {
         av[k] = fast_exp2(dl[k] * a2);
         bb[k] = u[k] * bn[k];
       }
+      __builtin_amdgcn_s_setprio(0);
       float f = 0.0f, p = 0.0f;
       float r = (DS & 2) ? sR[(DS & 2) ? n : 0][lane] : 0.0f;
       float g = (DS & 1) ? sG[(DS & 1) ? n : 0][lane] : 0.0f;
@@ -463,6 +467,7 @@ __global__ __launch_bounds__(64, 2) void k_bwd_main(Args<T> a) {
       const uint32_t s1 = static_cast<uint32_t>(min(n + 1, N - 1)) * nstride;
       a2_next = ld_buf(ra, voff4, s1, a.A2T);
       const sfloat* bn = scalar_ptr(bt + static_cast<size_t>(n) * 2 * SUB);
+      __builtin_amdgcn_s_setprio(1);  // back to 0 after the right-to-left walk
       // the previous state's terms: read here, added after the right-to-left walk, so that their way through LDS costs
       // no wait (state 0 reads what the tile before left and drops it)
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -507,10 +512,11 @@ __global__ __launch_bounds__(64, 2) void k_bwd_main(Args<T> a) {
         if (n > 0 && (lane & 1) == 0) pbc[(n - 1) * 2 * SUB + (lane >> 1)] = s;
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       }
+      __builtin_amdgcn_s_setprio(0);
       // left to right: f and p, and everything formed from the four states of a token
       float f = (DS & 1) ? sF[(DS & 1) ? n : 0][lane] : 0.0f;
       float p = (DS & 2) ? sP[(DS & 2) ? n : 0][lane] : 0.0f;
-      float dA = sA[n][lane];
+      float dA = sA[n][lane], dA1 = 0.0f;  // even and odd tokens: half the dependent chain
 #pragma unroll
       for (int k = 0; k < SUB; ++k) {
         float w, gs, hs;
@@ -528,7 +534,8 @@ __global__ __launch_bounds__(64, 2) void k_bwd_main(Args<T> a) {
           hs = (DS & 1) ? hs + rv[k] : rv[k];
         }
         dd[k] = fmaf(a2, w, dd[k]);
-        dA = fmaf(dl[k], w, dA);
+        if (k & 1) dA1 = fmaf(dl[k], w, dA1);
+        else dA = fmaf(dl[k], w, dA);
         du[k] = fmaf(bn[k], gs, du[k]);
         if (GATE) y[k] = fmaf(bn[SUB + k], hs, y[k]);
         sV[k][lane] = u[k] * gs;
@@ -536,12 +543,13 @@ __global__ __launch_bounds__(64, 2) void k_bwd_main(Args<T> a) {
       }
       if (DS & 1) sF[(DS & 1) ? n : 0][lane] = f;
       if (DS & 2) sP[(DS & 2) ? n : 0][lane] = p;
-      sA[n][lane] = dA;
+      sA[n][lane] = dA + dA1;
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     const float last = total(read_rows(sV, lane));
     if ((lane & 1) == 0) pbc[(N - 1) * 2 * SUB + (lane >> 1)] = last;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_s_setprio(1);  // through the next tile's start
     // the gradients of the token's own inputs
     float xr[SUB], dr[SUB];
     load_col(a.x + tile, bytes, voff, row_bytes, xr);
