@@ -9,10 +9,10 @@
 //
 // One read of u and of the two gradients, one write of du: an HBM stream with
 // about 50 operations per (token, channel), four of them exponentials and
-// reciprocals.  32768 x 4096 bf16: 264 us, against 215 us for its bytes at the
-// rate of a large copy; without the SiLU 230 us, so the vector work that the
-// stream does not cover is what is left (4-token steps at 4 wavefronts per SIMD:
-// the same time; a register limit for 4 wavefronts at 8 tokens spills: 1.0 ms).
+// reciprocals.  32768 x 4096 bf16: 229 us, against 215 us for its bytes at the
+// rate of a large copy (254 us while the wavefront's number was a vector value,
+// which made each access a loop over resources).  4-token steps 235 us; a register
+// limit for 4 wavefronts per SIMD 241.
 // A lane owns two channels and walks a tile of
 // tokens in steps of 8.  At step t0 it holds u[t0 .. t0 + 10]; from those 11
 // rows it forms dp_f of tokens t0 + 3 .. t0 + 10 and dp_r of t0 .. t0 + 7, the
@@ -105,7 +105,8 @@ template <typename T, bool ACT, int DIRS>
 __global__ __launch_bounds__(WAVES * 64) void k_conv_bwd(BwdArgs<T> a) {
   constexpr bool F = (DIRS & 1) != 0, R = (DIRS & 2) != 0;
   __shared__ float red[WAVES][kBwdSums][2][64];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  // the wavefront's number as a scalar: its tile's buffer resources must be uniform, or every access becomes a loop
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int64_t group = static_cast<int64_t>(blockIdx.x) / a.cblocks;
   const int64_t c0 = ((static_cast<int64_t>(blockIdx.x) - group * a.cblocks) * 64 + lane) * 2;
   const int64_t b = blockIdx.y;

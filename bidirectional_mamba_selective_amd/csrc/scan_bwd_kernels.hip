@@ -43,9 +43,10 @@
 // 671 (a tile's boundary states are read and written that much more often); lane swaps and DPP adds for the sums over
 // channels 550; the same sums on the matrix cores, exact in 4 x 4 blocks, 603; the next tile brought to LDS or to
 // registers during the current one 586 and 490; B and C loaded a state ahead into a second set of SGPRs 518.
-// The wavefronts of a SIMD take turns: the exponentials (in k_bwd_main the right-to-left walk and a tile's two ends too) run at a raised wave
-// priority, so that one wavefront's slow operations and dependent steps fall into the other's independent ones: 493 ->
-// 467 us, 247 -> 233 us.  k_bwd_carry 15 us, k_bwd_reduce 14 us and k_bwd_stage 5 us are streams of the workspace.
+// The wavefronts of a SIMD take turns: the exponentials (in k_bwd_main the right-to-left walk and a tile's two ends too)
+// run at a raised wave priority, so that one wavefront's slow operations and dependent steps fall into the other's
+// independent ones: 493 -> 467 us, 247 -> 233 us.  k_bwd_carry 15 us, k_bwd_reduce 14 us and k_bwd_stage 5 us are
+// streams of the workspace.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
