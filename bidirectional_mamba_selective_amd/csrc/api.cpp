@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "adaln_plan.h"
@@ -655,7 +656,8 @@ static int adaln_check(const void* branch, const float* post_weight, const float
   if (s != BIMAMBA_OK) return s;
   if (mod_rows != 1 && mod_rows != batch) return BIMAMBA_ERR_INVALID_ARGUMENT;
   if (flags & ~static_cast<uint32_t>(BIMAMBA_FLAG_RMS_NORM)) return BIMAMBA_ERR_INVALID_ARGUMENT;
-  if (!(eps > 0.0f) || !std::isfinite(eps)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  // the reciprocal square root takes a subnormal number for zero: a row of zeros would give 0 * inf
+  if (!(eps >= FLT_MIN) || !std::isfinite(eps)) return BIMAMBA_ERR_INVALID_ARGUMENT;
   if (!branch && (post_weight || gate)) return BIMAMBA_ERR_INVALID_ARGUMENT;
   return BIMAMBA_OK;
 }

@@ -402,7 +402,7 @@ int bimamba_conv1d_bidir_bwd(const void* dout_f, const void* dout_r, const void*
  *   be NULL with it.  Otherwise h is required; it may be x itself (the residual
  *   stream updated in place), and must not otherwise overlap an input.
  * Supported: d_model a multiple of 8 and at most 8192, 1 <= batch <= 65535, eps
- * positive and finite; every pointer 16-byte aligned; flags 0 or
+ * positive, finite and not subnormal; every pointer 16-byte aligned; flags 0 or
  * BIMAMBA_FLAG_RMS_NORM.  No workspace. */
 int bimamba_adaln_fwd(const void* x, const void* branch, const float* post_weight, const float* gate,
                       const float* gamma, const float* beta, void* h, void* out, int64_t batch, int64_t seqlen,

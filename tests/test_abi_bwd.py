@@ -162,6 +162,14 @@ def test_adaln_bwd_rejects(kw, want):
     assert call("bimamba_adaln_bwd", BWD, BWD_SIZES, kw) == want
 
 
+@pytest.mark.parametrize("eps", [1e-39, 1e-45])
+def test_adaln_rejects_a_subnormal_eps(eps):
+    """A reciprocal square root that takes subnormal numbers for zero would make NaN of a row of zeros."""
+    e = {"eps": ctypes.c_float(eps)}
+    assert call("bimamba_adaln_fwd", FWD, FWD_SIZES, e) == INV
+    assert call("bimamba_adaln_bwd", BWD, BWD_SIZES, e) == INV
+
+
 def test_workspace_bytes_of_the_stream_operators():
     f = _lib.bimamba_conv1d_bidir_bwd_workspace_bytes
     g = _lib.bimamba_adaln_bwd_workspace_bytes
