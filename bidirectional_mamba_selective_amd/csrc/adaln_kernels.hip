@@ -20,8 +20,9 @@
 // Both directions read each tensor once and write each result once; what bounds
 // them is HBM: 8 x 8192 rows of 2048 in bf16 take 216 us forward (1.07 GB, 5.0 TB/s)
 // and 330 us backward (1.61 GB, 4.9 TB/s), the rate of a large copy.  A few rows are
-// bound by the launch (32 rows: 3.2 us on the device).  A row sits in registers, 8 values a lane, across one to sixteen wavefronts; a
-// workgroup walks consecutive rows of one sequence, so gamma, beta, g and w are
+// bound by the launch (32 rows: 3.2 us on the device).  A row sits in registers,
+// 8 values a lane, across one to sixteen wavefronts; a workgroup walks consecutive
+// rows of one sequence, so gamma, beta, g and w are
 // loaded once per workgroup, and the next row's loads are in flight while the
 // current row is summed.  The column sums of the backward pass stay in registers
 // along that walk; each workgroup writes its partial sums once, and a second
