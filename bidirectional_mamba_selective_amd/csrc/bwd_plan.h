@@ -9,8 +9,8 @@
 
 namespace bimamba {
 
-// Wavefronts the chunking aims to give the main backward kernel: two per SIMD of a 256-CU part, all of them resident.
-constexpr int64_t kBwdTargetWaves = 2048;
+// Wavefronts of the main backward kernel that a 256-CU part holds at once: two per SIMD.
+constexpr int64_t kBwdResidentWaves = 2048;
 
 struct BwdPlan {
   int64_t batch, seqlen, d_inner, d_state;
@@ -26,6 +26,16 @@ struct BwdPlan {
   size_t total;
 };
 
+// Chunks per sequence for row_waves = batch * d_inner / 64 wavefronts per chunk: as many as stay resident together.  One
+// more would leave a second round of a few wavefronts, each walking a whole chunk on an idle chip (bf16, both directions,
+// N 16, rounded down against up: 5 x 2048 x 4096 896 against 1150 us, 8 x 1024 x 3840 672 against 874, 1 x 8192 x 3840 659
+// against 663).  Above half of the resident number that would be one chunk, a wavefront per sequence, and two rounds of
+// half the length are no longer than it: 20 x 512 x 4096 1121 against 1166 us, 31 x 512 x 4096 1358 either way.
+inline int64_t bwd_chunks(int64_t row_waves) {
+  const int64_t fit = kBwdResidentWaves / row_waves;
+  return fit >= 2 ? fit : row_waves < kBwdResidentWaves ? 2 : 1;
+}
+
 inline BwdPlan make_bwd_plan(int64_t batch, int64_t seqlen, int64_t d_inner, int64_t d_state) {
   BwdPlan p{};
   p.batch = batch;
@@ -33,7 +43,7 @@ inline BwdPlan make_bwd_plan(int64_t batch, int64_t seqlen, int64_t d_inner, int
   p.d_inner = d_inner;
   p.d_state = d_state;
   const int64_t row_waves = batch * (d_inner / kLanes);
-  const int64_t want_chunks = (kBwdTargetWaves + row_waves - 1) / row_waves;
+  const int64_t want_chunks = bwd_chunks(row_waves);
   int64_t chunk = (seqlen + want_chunks - 1) / want_chunks;
   chunk = ((chunk + kSub - 1) / kSub) * kSub;
   p.chunk = chunk;
