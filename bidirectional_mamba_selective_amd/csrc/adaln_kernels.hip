@@ -482,12 +482,12 @@ hipError_t bwd_typed(const AdalnArgs& in, const AdalnGrads& g, const Plan& p, vo
 }  // namespace
 
 hipError_t launch_adaln_fwd(const AdalnArgs& a, hipStream_t stream) {
-  const Plan p = make_plan(a.batch, a.seqlen, a.d_model, kFwdGroups);
+  const Plan p = fwd_plan(a.batch, a.seqlen, a.d_model);
   return a.io_dtype == 1 ? fwd_typed<bf16_t>(a, p, stream) : fwd_typed<float>(a, p, stream);
 }
 
 hipError_t launch_adaln_bwd(const AdalnArgs& a, const AdalnGrads& g, void* workspace, hipStream_t stream) {
-  const Plan p = make_plan(a.batch, a.seqlen, a.d_model, bwd_groups(waves_for(a.d_model)));
+  const Plan p = bwd_plan(a.batch, a.seqlen, a.d_model);
   return a.io_dtype == 1 ? bwd_typed<bf16_t>(a, g, p, workspace, stream)
                          : bwd_typed<float>(a, g, p, workspace, stream);
 }

@@ -24,10 +24,10 @@ inline int waves_for(int64_t d) {
   return w;
 }
 
-// Workgroups the backward pass aims at: as many as 256 CUs hold at once (its 132 to 157 registers allow 3 wavefronts per
-// SIMD, so 12 per CU), in one round: 8 x 8192 rows of 2048 in 320 + 11 us (kernel and partial sums) at 768, 373 + 15 us
-// at 1024 (a third of a round is left over), 335 + 8 us at 512.
-inline int64_t bwd_groups(int waves) {
+// Workgroups of the backward pass that 256 CUs hold at once: its 132 to 157 registers allow 3 wavefronts per SIMD, so 12 per
+// CU.  One round of them: 8 x 8192 rows of 2048 in 320 + 11 us (kernel and partial sums) at 768, 373 + 15 us at 1024 (a
+// third of a round is left over), 335 + 8 us at 512.
+inline int64_t bwd_resident(int waves) {
   const int per_wg = waves == 1 ? 4 : waves;
   return 256 * (per_wg >= 8 ? 1 : 12 / per_wg);
 }
@@ -42,17 +42,29 @@ struct Plan {
   size_t part_bytes;    // backward: partial column sums [batch][chunk][row group][kSums][d] fp32
 };
 
-inline Plan make_plan(int64_t batch, int64_t seqlen, int64_t d, int64_t want_groups) {
+// per_batch: workgroups per batch element at most.
+inline Plan make_plan(int64_t batch, int64_t seqlen, int64_t d, int64_t per_batch) {
   Plan p{};
   p.waves = waves_for(d);
   const int64_t g = row_groups(p.waves);
-  int64_t per_batch = (want_groups + batch - 1) / batch;
   int64_t rows = (seqlen + per_batch - 1) / per_batch;
   rows = (rows + g - 1) / g * g;
   p.rows_per_wg = rows;
   p.chunks = (seqlen + rows - 1) / rows;
   p.part_bytes = align256(static_cast<size_t>(batch) * p.chunks * g * kSums * d * sizeof(float));
   return p;
+}
+
+inline Plan fwd_plan(int64_t batch, int64_t seqlen, int64_t d) {
+  return make_plan(batch, seqlen, d, (kFwdGroups + batch - 1) / batch);
+}
+
+// Rounded down, so that the launch stays in its one round: rounded up, two workgroups past 256 walk their rows alone at the
+// end (3 x 8192 rows of 4096: 455 against 261 us; 7 x 8192 of 2048: 402 against 292).  One per sequence above half of the
+// resident number too: 512 x 128 of 2048 427 against 470 us, 129 x 256 of 4096 637 against 643.
+inline Plan bwd_plan(int64_t batch, int64_t seqlen, int64_t d) {
+  const int64_t fit = bwd_resident(waves_for(d)) / batch;
+  return make_plan(batch, seqlen, d, fit > 1 ? fit : 1);
 }
 
 }  // namespace adaln

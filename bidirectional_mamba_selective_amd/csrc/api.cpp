@@ -682,8 +682,7 @@ int bimamba_adaln_fwd(const void* x, const void* branch, const float* post_weigh
 
 size_t bimamba_adaln_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t d_model) {
   if (adaln_check_shape(batch, seqlen, d_model, BIMAMBA_F32) != BIMAMBA_OK) return 0;
-  namespace ad = bimamba::adaln;
-  return ad::make_plan(batch, seqlen, d_model, ad::bwd_groups(ad::waves_for(d_model))).part_bytes;
+  return bimamba::adaln::bwd_plan(batch, seqlen, d_model).part_bytes;
 }
 
 int bimamba_adaln_bwd(const void* dout, const void* dres, const void* h, const void* branch, const float* post_weight,

@@ -41,3 +41,29 @@ def test_scan_bwd_chunks_stay_in_one_round(L):
                 want = 2 if rows < SCAN_WAVES else 1
             per_chunk = -(-tiles // want)
             assert got == -(-tiles // per_chunk), (batch, L, d)
+
+
+def adaln_workgroups(batch, L, d):
+    """Workgroups of the backward pass: each keeps four column sums per row group (the workspace is padded to 256 bytes)."""
+    waves = 1
+    while waves * 512 < d:
+        waves *= 2
+    bytes_of = 4 * 4 * d * (4 if waves == 1 else 1)
+    return _lib.bimamba_adaln_bwd_workspace_bytes(batch, L, d) // bytes_of, waves
+
+
+@pytest.mark.parametrize("d", [64, 512, 1024, 1928, 2048, 4096, 8192])
+def test_adaln_bwd_workgroups_stay_in_one_round(d):
+    """No more workgroups than 256 CUs hold (12 wavefronts each, whole workgroups), except where there are more
+    sequences than that: then one a sequence."""
+    for L in (1, 7, 100, 1001, 2048, 8192):
+        for batch in list(range(1, 13)) + [40, 100, 129, 200, 257, 400, 512, 1000, 2000]:
+            got, waves = adaln_workgroups(batch, L, d)
+            per_wg = 4 if waves == 1 else waves
+            resident = 256 * max(1, 12 // per_wg)
+            assert got % batch == 0
+            assert got <= resident or got == batch, (batch, L, d, got)
+            # no fewer than the rows and that limit allow
+            rows = -(-L // max(1, resident // batch))
+            rows += -rows % (4 if waves == 1 else 1)
+            assert got == batch * -(-L // rows), (batch, L, d, got)
