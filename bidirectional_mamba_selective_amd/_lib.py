@@ -236,6 +236,8 @@ def _common(x, dt, A, B, C, D, z, dt_bias, out):
 def _stream(stream, device):
     torch = _torch()
     if stream is not None:
+        if stream.device != device:  # the kernels would run there with this device's addresses
+            raise ValueError(f"stream must be on {device}")
         return stream.cuda_stream
     if _raw_stream is not None:
         return _raw_stream(device.index)
