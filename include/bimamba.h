@@ -210,10 +210,10 @@ size_t bimamba_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t d
  * or dt_bias is NULL (= 0).  dz is required with the gate and must be NULL with
  * NO_GATE (z is then not read).  Shapes, dtypes, alignment (dA, dD, ddt_bias, dx,
  * ddt, dz 16 bytes; dB, dC one element) and the workspace (256-byte aligned,
- * contents ignored on entry) are as for bimamba_scan_fwd, and batch * d_state *
- * (seqlen rounded up to 16) must stay below 2^31 and batch * d_state * d_inner below
- * 2^32 (UNSUPPORTED otherwise).  No output may overlap an input, another output or
- * the workspace. */
+ * contents ignored on entry) are as for bimamba_scan_fwd, and
+ * 2 * batch * d_state * (seqlen rounded up to 16) + 4 * (d_state + 2) * d_inner + 1024
+ * and batch * d_state * d_inner + 256 must stay below 2^32 (UNSUPPORTED otherwise).
+ * No output may overlap an input, another output or the workspace. */
 int bimamba_scan_bwd(const void* dout, const void* x, const void* dt, const float* A, const void* B, const void* C,
                      const float* D, const void* z, const float* dt_bias, void* dx, void* ddt, float* dA, void* dB,
                      void* dC, float* dD, void* dz, float* ddt_bias, int64_t batch, int64_t seqlen, int64_t d_inner,

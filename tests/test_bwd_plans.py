@@ -67,3 +67,30 @@ def test_adaln_bwd_workgroups_stay_in_one_round(d):
             rows = -(-L // max(1, resident // batch))
             rows += -rows % (4 if waves == 1 else 1)
             assert got == batch * -(-L // rows), (batch, L, d, got)
+
+
+def scan_fits(batch, L, d, n):
+    """The limits that include/bimamba.h states for bimamba_scan_bwd beside those of the forward call."""
+    tokens = -(-L // TILE) * TILE
+    return 2 * batch * n * tokens + 4 * (n + 2) * d + 1024 < 2 ** 32 and batch * n * d + 256 < 2 ** 32
+
+
+@pytest.mark.parametrize("batch,L,d,n,fits", [
+    (2, 1073741360, 64, 1, True),
+    (2, 1073741361, 64, 1, False),   # rounded up to 1073741376: 2 * 1 * that is still below 2^31
+    (1, 131857920, 1 << 20, 16, True),
+    (1, 131900000, 1 << 20, 16, False),  # the channels' term alone decides
+    (8, 16, 33554368, 16, True),
+    (9, 16, 33554368, 16, False),
+])
+def test_scan_bwd_limits_are_the_documented_ones(batch, L, d, n, fits):
+    assert scan_fits(batch, L, d, n) == fits
+    assert (_lib.bimamba_scan_bwd_workspace_bytes(batch, L, d, n) > 0) == fits
+
+
+def test_the_header_states_the_limits():
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "bimamba.h")
+    with open(path) as f:
+        text = " ".join(line.strip(" *\n") for line in f)
+    assert "2 * batch * d_state * (seqlen rounded up to 16) + 4 * (d_state + 2) * d_inner + 1024" in text
+    assert "batch * d_state * d_inner + 256" in text
