@@ -184,7 +184,7 @@ __device__ __forceinline__ void centre(float (&v)[V], const Cols& c, float mu) {
   for (int e = 0; e < V; ++e) v[e] = c.on ? v[e] - mu : 0.0f;
 }
 
-// 1 / sqrt(v): the hardware's estimate (1 ulp) is what an fp32 reciprocal root rounds to
+// 1 / sqrt(v) by the hardware's estimate, within 1 ulp (2^-23 relative) of the root
 __device__ __forceinline__ float rsqrt_f32(float v) { return __builtin_amdgcn_rsqf(v); }
 
 template <typename T>
