@@ -9,10 +9,11 @@
 //
 // One read of u and of the two gradients, one write of du: an HBM stream with
 // about 50 operations per (token, channel), four of them exponentials and
-// reciprocals.  32768 x 4096 bf16: 229 us, against 215 us for its bytes at the
-// rate of a large copy (254 us while the wavefront's number was a vector value,
-// which made each access a loop over resources).  4-token steps 235 us; a register
-// limit for 4 wavefronts per SIMD 241.
+// reciprocals.  32768 x 4096 bf16: 229 us a call (kernel 221 and 228 on two cards,
+// the sum of the partial sums 6), against 215 us for its bytes at the rate of a
+// large copy.  254 us while the wavefront's number was a vector value, which made
+// each access a loop over resources; 4-token steps 235 us; a register limit for 4
+// wavefronts per SIMD 241.
 // A lane owns two channels and walks a tile of
 // tokens in steps of 8.  At step t0 it holds u[t0 .. t0 + 10]; from those 11
 // rows it forms dp_f of tokens t0 + 3 .. t0 + 10 and dp_r of t0 .. t0 + 7, the

@@ -36,17 +36,19 @@
 // lanes a row while the next state is under way.
 //
 // What bounds it, at 8192 tokens x 4096 channels x 16 states, bf16, both directions (0.67 ms a call; its tensors alone
-// would stream in 0.09 ms): vector issue.  k_bwd_main, 467 us, runs 28 operations per (token, channel, state) and
-// k_bwd_summary, 233 us, 12; at the 2.3 clocks that independent operations take that is 0.4 ms.  The rest: scalar
+// would stream in 0.09 ms): vector issue.  k_bwd_main, 415 us, runs 28 operations per (token, channel, state) and
+// k_bwd_summary, 210 us, 12; at the 2.3 clocks that independent operations take that is 0.4 ms.  The rest: scalar
 // operands back to back (3.5 clocks), exponentials (7), and the loads at a tile's two ends, which two wavefronts per SIMD
-// do not cover.  Measured and not kept for k_bwd_main: tiles of 12 tokens at 3 wavefronts per SIMD 552 us and of 8 at 4
+// do not cover.  k_bwd_carry 14 us, k_bwd_reduce 14 us and k_bwd_stage 5 us are streams of the workspace.  These are
+// medians of 200 calls once the clock has settled (two cards differ by 3 %).  The figures from here on are of 20 calls
+// before that, where the kept kernels take 467 and 233 us; the next five stood beside kept forms of 552 to 490.
+// Measured and not kept for k_bwd_main: tiles of 12 tokens at 3 wavefronts per SIMD 552 us and of 8 at 4
 // 671 (a tile's boundary states are read and written that much more often); lane swaps and DPP adds for the sums over
 // channels 550; the same sums on the matrix cores, exact in 4 x 4 blocks, 603; the next tile brought to LDS or to
 // registers during the current one 586 and 490; B and C loaded a state ahead into a second set of SGPRs 518.
 // The wavefronts of a SIMD take turns: the exponentials (in k_bwd_main the right-to-left walk and a tile's two ends too)
 // run at a raised wave priority, so that one wavefront's slow operations and dependent steps fall into the other's
-// independent ones: 493 -> 467 us, 247 -> 233 us.  k_bwd_carry 15 us, k_bwd_reduce 14 us and k_bwd_stage 5 us are
-// streams of the workspace.
+// independent ones: 493 -> 467 us, 247 -> 233 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
