@@ -16,10 +16,16 @@ from ._lib import (  # noqa: F401
     bimamba_adaln_bwd,
     bimamba_adaln_bwd_workspace_bytes,
     bimamba_adaln_fwd,
+    bimamba_adaln_fwd_fp8,
     bimamba_conv1d_bidir,
     bimamba_conv1d_bidir_bwd,
     bimamba_conv1d_bidir_bwd_workspace_bytes,
     bimamba_conv1d_block,
+    bimamba_delta_bwd,
+    bimamba_delta_bwd_workspace_bytes,
+    bimamba_delta_fwd,
+    bimamba_delta_fwd_workspace_bytes,
+    bimamba_proj_fp8,
     bimamba_scan_block,
     bimamba_scan_block_workspace_bytes,
     bimamba_scan_bwd,

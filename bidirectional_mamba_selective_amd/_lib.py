@@ -54,8 +54,14 @@ EXPORTED = (
     "bimamba_conv1d_bidir_bwd_workspace_bytes",
     "bimamba_conv1d_bidir_bwd",
     "bimamba_adaln_fwd",
+    "bimamba_adaln_fwd_fp8",
     "bimamba_adaln_bwd_workspace_bytes",
     "bimamba_adaln_bwd",
+    "bimamba_proj_fp8",
+    "bimamba_delta_fwd_workspace_bytes",
+    "bimamba_delta_fwd",
+    "bimamba_delta_bwd_workspace_bytes",
+    "bimamba_delta_bwd",
 )
 
 _lib = None
@@ -125,11 +131,22 @@ def load() -> ctypes.CDLL:
     lib.bimamba_conv1d_bidir_bwd.argtypes = [vp] * 12 + [i64] * 4 + [ctypes.c_int, ctypes.c_uint32, vp, sz, vp]
     lib.bimamba_adaln_fwd.restype = ctypes.c_int
     lib.bimamba_adaln_fwd.argtypes = [vp] * 8 + [i64] * 4 + [ctypes.c_float, ctypes.c_int, ctypes.c_uint32, vp]
+    lib.bimamba_adaln_fwd_fp8.restype = ctypes.c_int
+    lib.bimamba_adaln_fwd_fp8.argtypes = [vp] * 9 + [i64] * 4 + [ctypes.c_float, ctypes.c_int, ctypes.c_uint32, vp]
     lib.bimamba_adaln_bwd_workspace_bytes.restype = sz
     lib.bimamba_adaln_bwd_workspace_bytes.argtypes = [i64] * 3
     lib.bimamba_adaln_bwd.restype = ctypes.c_int
     lib.bimamba_adaln_bwd.argtypes = [vp] * 13 + [i64] * 4 + [ctypes.c_float, ctypes.c_int, ctypes.c_uint32, vp, sz,
                                                               vp]
+    lib.bimamba_proj_fp8.restype = ctypes.c_int
+    lib.bimamba_proj_fp8.argtypes = [vp] * 5 + [i64] * 3 + [ctypes.c_int, vp]
+    for name, pointers in (("bimamba_delta_fwd", 10), ("bimamba_delta_bwd", 18)):
+        size = getattr(lib, name + "_workspace_bytes")
+        size.restype = sz
+        size.argtypes = [i64] * 6
+        entry = getattr(lib, name)
+        entry.restype = ctypes.c_int
+        entry.argtypes = [vp] * pointers + [i64] * 6 + [ctypes.c_float, ctypes.c_int, ctypes.c_uint32, vp, sz, vp]
     _lib = lib
     return lib
 
@@ -725,6 +742,32 @@ def bimamba_adaln_fwd(x, gamma=None, beta=None, branch=None, post_weight=None, g
     return (x if branch is None else h), out
 
 
+def bimamba_adaln_fwd_fp8(x, gamma=None, beta=None, branch=None, post_weight=None, gate=None, eps: float = 1e-5,
+                          flags: int = 0, h=None, out=None, scales=None, stream=None):
+    """bimamba_adaln_fwd with out in 8 bits (torch.float8_e4m3fn) and one fp32 scale per row and 128 columns: the norm's
+    value is out * scale.  Returns (h, out, scales), scales [batch, seqlen, d_model / 128]; d_model is a multiple of 128."""
+    torch = _torch()
+    lib = load()
+    dev = x.device
+    with _at(dev, stream):
+        nb, L, nd, rows = _adaln_common(x, "x", gamma, beta, branch, post_weight, gate)
+        if branch is not None and h is None:
+            h = torch.empty_like(x)
+        if out is None:
+            out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+        if scales is None:
+            scales = torch.empty((nb, L, nd // 128), dtype=torch.float32, device=dev)
+        _check(h, "h", x.shape, x.dtype, dev)
+        _check(out, "out", x.shape, torch.float8_e4m3fn, dev)
+        _check(scales, "scales", (nb, L, nd // 128), torch.float32, dev)
+        st = lib.bimamba_adaln_fwd_fp8(_ptr(x), _ptr(branch), _ptr(post_weight), _ptr(gate), _ptr(gamma), _ptr(beta),
+                                       _ptr(h), _ptr(out), _ptr(scales), nb, L, nd, rows, eps, _io_dtype(x), flags,
+                                       _stream(stream, dev))
+    if st != BIMAMBA_OK:
+        raise BimambaError(st, "bimamba_adaln_fwd_fp8")
+    return (x if branch is None else h), out, scales
+
+
 def bimamba_adaln_bwd_workspace_bytes(batch: int, seqlen: int, d_model: int) -> int:
     return int(load().bimamba_adaln_bwd_workspace_bytes(batch, seqlen, d_model))
 
@@ -751,4 +794,108 @@ def bimamba_adaln_bwd(dout, dres, h, gamma=None, beta=None, branch=None, post_we
                                    _stream(stream, dev))
     if st != BIMAMBA_OK:
         raise BimambaError(st, "bimamba_adaln_bwd")
+    return g
+
+
+def bimamba_proj_fp8(x, x_scales, w, w_scales, out=None, out_dtype=None, stream=None):
+    """The product of 8-bit rows and weights with block scales: out[..., n] = sum over blocks j of 128 inputs of
+    x_scales[..., j] * w_scales[n // 128, j] * (x . w[n] in that block).  x [batch, seqlen, d_in] and w [d_out, d_in] are
+    torch.float8_e4m3fn, x_scales [batch, seqlen, d_in / 128] and w_scales [ceil(d_out / 128), d_in / 128] fp32 (x and
+    x_scales as bimamba_adaln_fwd_fp8 returns them).  Returns out [batch, seqlen, d_out], of out_dtype (bf16 by default)."""
+    torch = _torch()
+    lib = load()
+    dev, f8 = x.device, torch.float8_e4m3fn
+    if x.dim() != 3 or w.dim() != 2:
+        raise ValueError("x must be [batch, seqlen, d_in] and w [d_out, d_in]")
+    nb, L, k = x.shape
+    n = w.shape[0]
+    with _at(dev, stream):
+        _check(x, "x", (nb, L, k), f8, dev)
+        _check(w, "w", (n, k), f8, dev)
+        _check(x_scales, "x_scales", (nb, L, k // 128), torch.float32, dev)
+        _check(w_scales, "w_scales", ((n + 127) // 128, k // 128), torch.float32, dev)
+        if out is None:
+            out = torch.empty((nb, L, n), dtype=out_dtype or torch.bfloat16, device=dev)
+        _check(out, "out", (nb, L, n), out_dtype or out.dtype, dev)
+        st = lib.bimamba_proj_fp8(_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), _ptr(out), nb * L, n, k,
+                                  _io_dtype(out), _stream(stream, dev))
+    if st != BIMAMBA_OK:
+        raise BimambaError(st, "bimamba_proj_fp8")
+    return out
+
+
+def bimamba_delta_fwd_workspace_bytes(batch: int, seqlen: int, nheads_k: int, nheads: int, headdim_k: int,
+                                      headdim_v: int) -> int:
+    return int(load().bimamba_delta_fwd_workspace_bytes(batch, seqlen, nheads_k, nheads, headdim_k, headdim_v))
+
+
+def bimamba_delta_bwd_workspace_bytes(batch: int, seqlen: int, nheads_k: int, nheads: int, headdim_k: int,
+                                      headdim_v: int) -> int:
+    return int(load().bimamba_delta_bwd_workspace_bytes(batch, seqlen, nheads_k, nheads, headdim_k, headdim_v))
+
+
+def _delta_common(q, k, v, dt, A, b, dt_bias, h_in):
+    torch = _torch()
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be [batch, seqlen, nheads_k, headdim_k] and v [batch, seqlen, nheads, headdim_v]")
+    nb, L, hk, dk = q.shape
+    nh, dv = v.shape[2:]
+    dev, io, f32 = q.device, q.dtype, torch.float32
+    _check(q, "q", (nb, L, hk, dk), io, dev)
+    _check(k, "k", (nb, L, hk, dk), io, dev)
+    _check(v, "v", (nb, L, nh, dv), io, dev)
+    _check(dt, "dt", (nb, L, nh), io, dev)
+    _check(b, "b", (nb, L, nh), io, dev)
+    _check(A, "A", (nh,), f32, dev)
+    _check(dt_bias, "dt_bias", (nh,), f32, dev)
+    _check(h_in, "h_in", (nb, nh, dk, dv), f32, dev)
+    return nb, L, hk, nh, dk, dv
+
+
+def bimamba_delta_fwd(q, k, v, dt, A, b, dt_bias=None, h_in=None, h_out=None, out=None, scale=None,
+                      flags: int = FLAG_FWD_ONLY, workspace=None, stream=None):
+    """One direction of the gated delta rule (FLAG_FWD_ONLY or FLAG_REV_ONLY): per head, with a = exp(softplus(dt +
+    dt_bias) * A) and beta = sigmoid(b), H = a * H_before, H_t = H + beta * outer(k, v - H^T k), out = scale * H_t^T q.
+    q, k [batch, seqlen, nheads_k, headdim_k], v [batch, seqlen, nheads, headdim_v], dt, b [batch, seqlen, nheads] bf16;
+    A, dt_bias [nheads] fp32; h_in, h_out [batch, nheads, headdim_k, headdim_v] fp32 (h_out may be h_in): the states
+    before and after the call's tokens.  scale is 1 / sqrt(headdim_k) unless given.  Returns out, like v."""
+    torch = _torch()
+    lib = load()
+    dev = q.device
+    with _at(dev, stream):
+        nb, L, hk, nh, dk, dv = _delta_common(q, k, v, dt, A, b, dt_bias, h_in)
+        _check(h_out, "h_out", (nb, nh, dk, dv), torch.float32, dev)
+        if out is None:
+            out = torch.empty_like(v)
+        _check(out, "out", v.shape, v.dtype, dev)
+        workspace, wbytes = _workspace(workspace, lib.bimamba_delta_fwd_workspace_bytes(nb, L, hk, nh, dk, dv), dev)
+        st = lib.bimamba_delta_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A), _ptr(b), _ptr(dt_bias), _ptr(h_in),
+                                   _ptr(h_out), _ptr(out), nb, L, hk, nh, dk, dv, dk ** -0.5 if scale is None else scale,
+                                   _io_dtype(q), flags, _ptr(workspace), wbytes, _stream(stream, dev))
+    if st != BIMAMBA_OK:
+        raise BimambaError(st, "bimamba_delta_fwd")
+    return out
+
+
+def bimamba_delta_bwd(dout, q, k, v, dt, A, b, dt_bias=None, h_in=None, dh_out=None, scale=None,
+                      flags: int = FLAG_FWD_ONLY, grads=None, workspace=None, stream=None):
+    """Gradients of bimamba_delta_fwd's inputs for dout (of out) and dh_out (of h_out, None = 0).  Returns a dict with keys
+    q, k, v, dt, A, b, dt_bias, h_in, None for an input that was not given.  grads may hold tensors to write into;
+    grads["h_in"] may be dh_out."""
+    torch = _torch()
+    lib = load()
+    dev = q.device
+    with _at(dev, stream):
+        nb, L, hk, nh, dk, dv = _delta_common(q, k, v, dt, A, b, dt_bias, h_in)
+        _check(dout, "dout", v.shape, v.dtype, dev)
+        _check(dh_out, "dh_out", (nb, nh, dk, dv), torch.float32, dev)
+        g = _grads(grads, {"q": q, "k": k, "v": v, "dt": dt, "A": A, "b": b, "dt_bias": dt_bias, "h_in": h_in})
+        workspace, wbytes = _workspace(workspace, lib.bimamba_delta_bwd_workspace_bytes(nb, L, hk, nh, dk, dv), dev)
+        st = lib.bimamba_delta_bwd(_ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A), _ptr(b), _ptr(dt_bias),
+                                   _ptr(h_in), _ptr(dh_out), _ptr(g["q"]), _ptr(g["k"]), _ptr(g["v"]), _ptr(g["dt"]),
+                                   _ptr(g["A"]), _ptr(g["b"]), _ptr(g["dt_bias"]), _ptr(g["h_in"]), nb, L, hk, nh, dk,
+                                   dv, dk ** -0.5 if scale is None else scale, _io_dtype(q), flags, _ptr(workspace),
+                                   wbytes, _stream(stream, dev))
+    if st != BIMAMBA_OK:
+        raise BimambaError(st, "bimamba_delta_bwd")
     return g

@@ -44,6 +44,7 @@ constexpr int V = static_cast<int>(kVec);
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -196,13 +197,44 @@ struct FwdArgs {
   const float* gamma;  // null: 1
   const float* beta;   // null: 0
   T* h;                // null without a branch; may be x
-  T* out;
+  void* out;           // T, or 8 bits
+  float* scales;       // 8 bits only: [row][d / kScaleCols]
   int64_t L, d, rows_per_wg, mod_stride;  // mod_stride: d, or 0 where one gamma, beta, g serves every sequence
   float inv_d, eps;
   int rms;
 };
 
-template <typename T, int WPR>
+template <int CTRL>
+__device__ __forceinline__ float max_dpp(float v) {
+  return fmaxf(v, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xf, 0xf, true)));
+}
+
+// 8 values of a row as e4m3 (round to nearest even), with one scale for the 128 columns that 16 lanes hold:
+// scale = max(largest magnitude, 2^-100) / 448.  The magnitude's floor keeps the scale and its reciprocal normal numbers,
+// so a block of zeros gives zeros.  The maximum passes over a NaN; the value itself stays one.
+__device__ __forceinline__ void put_fp8(const float (&v)[V], uint8_t* out, float* scales, int64_t row, int64_t d,
+                                        const Cols& c) {
+  float m = fabsf(v[0]);
+#pragma unroll
+  for (int e = 1; e < V; ++e) m = fmaxf(m, fabsf(v[e]));
+  m = max_dpp<0xB1>(m);   // quad_perm [1,0,3,2]
+  m = max_dpp<0x4E>(m);   // quad_perm [2,3,0,1]
+  m = max_dpp<0x141>(m);  // row_half_mirror
+  m = max_dpp<0x140>(m);  // row_mirror
+  const float s = fmaxf(m, 0x1p-100f) / 448.0f;
+  const float r = 1.0f / s;
+  int lo = 0, hi = 0;
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * r, v[1] * r, lo, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * r, v[3] * r, lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * r, v[5] * r, hi, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6] * r, v[7] * r, hi, true);
+  if (!c.on) return;
+  __builtin_nontemporal_store(u32x2{static_cast<uint32_t>(lo), static_cast<uint32_t>(hi)},
+                              reinterpret_cast<u32x2*>(out + row * d + c.at));
+  if ((threadIdx.x & 15) == 0) scales[row * (d / kScaleCols) + c.at / kScaleCols] = s;
+}
+
+template <typename T, int WPR, bool FP8>
 __global__ __launch_bounds__(WPR == 1 ? 256 : WPR * 64) void k_adaln_fwd(FwdArgs<T> a) {
   constexpr int G = WPR == 1 ? 4 : 1;
   __shared__ RowSums<WPR, 1> sm;
@@ -267,7 +299,8 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : WPR * 64) void k_adaln_fwd(FwdArgs
     const float rs = rsqrt_f32(fmaf(s[0], a.inv_d, a.eps));
 #pragma unroll
     for (int i = 0; i < V; ++i) h[i] = fmaf(h[i] * rs, gamma[i], beta[i]);
-    put_row<T>(h, a.out, base + r, a.d, c);
+    if constexpr (FP8) put_fp8(h, static_cast<uint8_t*>(a.out), a.scales, base + r, a.d, c);
+    else put_row<T>(h, static_cast<T*>(a.out), base + r, a.d, c);
   }
 }
 
@@ -447,12 +480,14 @@ void with_waves(int waves, F&& f) {
 template <typename T>
 hipError_t fwd_typed(const AdalnArgs& in, const Plan& p, hipStream_t stream) {
   FwdArgs<T> a{static_cast<const T*>(in.x), static_cast<const T*>(in.branch), in.post_weight, in.gate, in.gamma, in.beta,
-               static_cast<T*>(in.h), static_cast<T*>(in.out), in.seqlen, in.d_model, p.rows_per_wg,
+               static_cast<T*>(in.h), in.out, in.scales, in.seqlen, in.d_model, p.rows_per_wg,
                in.mod_rows == 1 ? 0 : in.d_model, 1.0f / static_cast<float>(in.d_model), in.eps, in.rms};
   const dim3 grid(static_cast<unsigned>(p.chunks), static_cast<unsigned>(in.batch));
   with_waves(p.waves, [&](auto w) {
     constexpr int W = decltype(w)::value;
-    hipLaunchKernelGGL((k_adaln_fwd<T, W>), grid, dim3(W == 1 ? 256 : W * 64), 0, stream, a);
+    const dim3 block(W == 1 ? 256 : W * 64);
+    if (in.scales) hipLaunchKernelGGL((k_adaln_fwd<T, W, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((k_adaln_fwd<T, W, false>), grid, block, 0, stream, a);
   });
   return hipGetLastError();
 }

@@ -13,6 +13,7 @@ namespace adaln {
 
 constexpr int64_t kVec = 8;           // values per thread and vector load
 constexpr int64_t kMaxWidth = 8192;   // widest row: 16 wavefronts, one vector per lane
+constexpr int64_t kScaleCols = 128;   // columns that share a scale of the 8-bit output: 16 lanes
 constexpr int64_t kFwdGroups = 2048;  // workgroups the forward pass aims at (8 per CU)
 constexpr int kSums = 4;              // column sums of the backward pass: dgamma, dbeta, dgate, dpost_weight
 

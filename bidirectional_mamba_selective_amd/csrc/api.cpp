@@ -11,6 +11,7 @@
 #include "adaln_plan.h"
 #include "bwd_plan.h"
 #include "conv_bwd_plan.h"
+#include "delta_plan.h"
 #include "launch.h"
 #include "plan.h"
 
@@ -680,6 +681,27 @@ int bimamba_adaln_fwd(const void* x, const void* branch, const float* post_weigh
   return map_hip(bimamba::adaln::launch_adaln_fwd(a, stream));
 }
 
+int bimamba_adaln_fwd_fp8(const void* x, const void* branch, const float* post_weight, const float* gate,
+                          const float* gamma, const float* beta, void* h, void* out, float* scales, int64_t batch,
+                          int64_t seqlen, int64_t d_model, int64_t mod_rows, float eps, int io_dtype, uint32_t flags,
+                          hipStream_t stream) {
+  const int s = adaln_check(branch, post_weight, gate, batch, seqlen, d_model, mod_rows, eps, io_dtype, flags);
+  if (s != BIMAMBA_OK) return s;
+  if (d_model % bimamba::adaln::kScaleCols != 0) return BIMAMBA_ERR_UNSUPPORTED;
+  if (!x || !out || !scales || (branch != nullptr) != (h != nullptr)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const size_t n = static_cast<size_t>(batch) * seqlen * d_model;
+  const size_t act = n * (io_dtype == BIMAMBA_BF16 ? 2 : 4);
+  const size_t mod = static_cast<size_t>(mod_rows) * d_model * 4, vec = static_cast<size_t>(d_model) * 4;
+  if (!aligned(x, 16)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const Buf v[] = {{h, act, 16}, {out, n, 16}, {scales, n / bimamba::adaln::kScaleCols * 4, 4},
+                   {h == x ? nullptr : x, act, 16}, {branch, act, 16}, {post_weight, vec, 16}, {gate, mod, 16},
+                   {gamma, mod, 16}, {beta, mod, 16}};
+  if (!buffers_ok(v, static_cast<int>(sizeof(v) / sizeof(v[0])), 3)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  bimamba::adaln::AdalnArgs a{x, branch, post_weight, gate, gamma, beta, h, out, batch, seqlen, d_model, mod_rows, eps,
+                              (flags & BIMAMBA_FLAG_RMS_NORM) ? 1 : 0, io_dtype, scales};
+  return map_hip(bimamba::adaln::launch_adaln_fwd(a, stream));
+}
+
 size_t bimamba_adaln_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t d_model) {
   if (adaln_check_shape(batch, seqlen, d_model, BIMAMBA_F32) != BIMAMBA_OK) return 0;
   return bimamba::adaln::bwd_plan(batch, seqlen, d_model).part_bytes;
@@ -709,6 +731,126 @@ int bimamba_adaln_bwd(const void* dout, const void* dres, const void* h, const v
                                     io_dtype};
   const bimamba::adaln::AdalnGrads g{dout, dres, dx, dbranch, dpost_weight, dgate, dgamma, dbeta};
   return map_hip(bimamba::adaln::launch_adaln_bwd(a, g, workspace, stream));
+}
+
+// ---- Product in 8 bits with block scales ----
+
+int bimamba_proj_fp8(const void* x, const float* x_scales, const void* w, const float* w_scales, void* out,
+                     int64_t rows, int64_t d_out, int64_t d_in, int out_dtype, hipStream_t stream) {
+  if (rows <= 0 || d_out <= 0 || d_in <= 0) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  if (out_dtype != BIMAMBA_F32 && out_dtype != BIMAMBA_BF16) return BIMAMBA_ERR_UNSUPPORTED;
+  if (d_in % 128 != 0 || d_out % 8 != 0) return BIMAMBA_ERR_UNSUPPORTED;
+  // tiles of 128 rows and 128 outputs go into a grid of 2^31 - 1 by 65535; byte counts stay below 2^53
+  if (d_out > (int64_t{1} << 22) || d_in > (int64_t{1} << 22) || rows > (int64_t{1} << 31))
+    return BIMAMBA_ERR_UNSUPPORTED;
+  if (!x || !x_scales || !w || !w_scales || !out) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const size_t kb = static_cast<size_t>(d_in) / 128;
+  const Buf v[] = {{out, static_cast<size_t>(rows) * d_out * (out_dtype == BIMAMBA_BF16 ? 2 : 4), 16},
+                   {x, static_cast<size_t>(rows) * d_in, 16},
+                   {x_scales, static_cast<size_t>(rows) * kb * 4, 4},
+                   {w, static_cast<size_t>(d_out) * d_in, 16},
+                   {w_scales, static_cast<size_t>((d_out + 127) / 128) * kb * 4, 4}};
+  if (!buffers_ok(v, 5, 1)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const bimamba::proj::ProjArgs a{x, x_scales, w, w_scales, out, rows, d_out, d_in, out_dtype};
+  return map_hip(bimamba::proj::launch_proj(a, stream));
+}
+
+// ---- Gated delta rule ----
+
+static int delta_check_shape(int64_t batch, int64_t seqlen, int64_t hk, int64_t heads, int64_t dk, int64_t dv,
+                             int io_dtype) {
+  if (batch <= 0 || seqlen <= 0 || hk <= 0 || heads <= 0 || dk <= 0 || dv <= 0) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  if (heads % hk != 0) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  if (io_dtype != BIMAMBA_BF16) return BIMAMBA_ERR_UNSUPPORTED;
+  if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128)) return BIMAMBA_ERR_UNSUPPORTED;
+  // heads and batch elements are grid dimensions of 16 bits; one workgroup per 16 columns of a head, in whole runs of
+  // eight heads, in a grid of fewer than 2^32 threads
+  if (batch > 65535 || heads > 65535 || seqlen > INT32_MAX / 2) return BIMAMBA_ERR_UNSUPPORTED;
+  if (static_cast<double>(batch) * heads > 1.0e6) return BIMAMBA_ERR_UNSUPPORTED;
+  // a chunk, head and batch element per workgroup of 256 threads
+  if (static_cast<double>((seqlen + 63) / 64) * 256 > 4.0e9) return BIMAMBA_ERR_UNSUPPORTED;
+  return BIMAMBA_OK;
+}
+
+static int delta_check_args(const void* q, const void* k, const void* v, const void* dt, const float* A, const void* b,
+                            float scale, uint32_t flags) {
+  if (flags != BIMAMBA_FLAG_FWD_ONLY && flags != BIMAMBA_FLAG_REV_ONLY) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  if (!q || !k || !v || !dt || !A || !b || !std::isfinite(scale)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  return BIMAMBA_OK;
+}
+
+size_t bimamba_delta_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads_k, int64_t nheads,
+                                         int64_t headdim_k, int64_t headdim_v) {
+  if (delta_check_shape(batch, seqlen, nheads_k, nheads, headdim_k, headdim_v, BIMAMBA_BF16) != BIMAMBA_OK) return 0;
+  return bimamba::delta::make_fwd_plan(batch, seqlen, nheads_k, nheads, headdim_k, headdim_v).total;
+}
+
+int bimamba_delta_fwd(const void* q, const void* k, const void* v, const void* dt, const float* A, const void* b,
+                      const float* dt_bias, const float* h_in, float* h_out, void* out, int64_t batch, int64_t seqlen,
+                      int64_t nheads_k, int64_t nheads, int64_t headdim_k, int64_t headdim_v, float scale, int io_dtype,
+                      uint32_t flags, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  int s = delta_check_shape(batch, seqlen, nheads_k, nheads, headdim_k, headdim_v, io_dtype);
+  if (s != BIMAMBA_OK) return s;
+  s = delta_check_args(q, k, v, dt, A, b, scale, flags);
+  if (s != BIMAMBA_OK) return s;
+  if (!out) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const bimamba::delta::Plan p =
+      bimamba::delta::make_fwd_plan(batch, seqlen, nheads_k, nheads, headdim_k, headdim_v);
+  const bool step = p.total == 0;
+  if (!step) {
+    if (workspace_bytes < p.total) return BIMAMBA_ERR_WORKSPACE_TOO_SMALL;
+    if (!workspace) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  }
+  const size_t rows = static_cast<size_t>(batch) * seqlen;
+  const size_t key = rows * nheads_k * headdim_k * 2, val = rows * nheads * headdim_v * 2, tok = rows * nheads * 2;
+  const size_t st = static_cast<size_t>(batch) * nheads * headdim_k * headdim_v * 4, par = static_cast<size_t>(nheads) * 4;
+  // h_out may be h_in itself: each value of the state is read before it is written, by the wavefront that writes it
+  if (h_in && !aligned(h_in, 16)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const Buf bufs[] = {{out, val, 16}, {h_out, st, 16}, {step ? nullptr : workspace, p.total, 256},
+                      {q, key, 16}, {k, key, 16}, {v, val, 16}, {dt, tok, 2}, {A, par, 4}, {b, tok, 2},
+                      {dt_bias, par, 4}, {h_in == h_out ? nullptr : h_in, st, 16}};
+  if (!buffers_ok(bufs, static_cast<int>(sizeof(bufs) / sizeof(bufs[0])), 3)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const bimamba::delta::DeltaArgs a{q, k, v, dt, A, b, dt_bias, h_in, h_out, out, batch, seqlen, nheads_k, nheads,
+                                    headdim_k, headdim_v, scale, (flags & BIMAMBA_FLAG_REV_ONLY) ? 1 : 0};
+  return map_hip(step ? bimamba::delta::launch_delta_step(a, stream)
+                      : bimamba::delta::launch_delta_fwd(a, p, workspace, stream));
+}
+
+size_t bimamba_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads_k, int64_t nheads,
+                                         int64_t headdim_k, int64_t headdim_v) {
+  if (delta_check_shape(batch, seqlen, nheads_k, nheads, headdim_k, headdim_v, BIMAMBA_BF16) != BIMAMBA_OK) return 0;
+  return bimamba::delta::make_bwd_plan(batch, seqlen, nheads_k, nheads, headdim_k, headdim_v).total;
+}
+
+int bimamba_delta_bwd(const void* dout, const void* q, const void* k, const void* v, const void* dt, const float* A,
+                      const void* b, const float* dt_bias, const float* h_in, const float* dh_out, void* dq, void* dk,
+                      void* dv, void* ddt, float* dA, void* db, float* ddt_bias, float* dh_in, int64_t batch,
+                      int64_t seqlen, int64_t nheads_k, int64_t nheads, int64_t headdim_k, int64_t headdim_v,
+                      float scale, int io_dtype, uint32_t flags, void* workspace, size_t workspace_bytes,
+                      hipStream_t stream) {
+  int s = delta_check_shape(batch, seqlen, nheads_k, nheads, headdim_k, headdim_v, io_dtype);
+  if (s != BIMAMBA_OK) return s;
+  s = delta_check_args(q, k, v, dt, A, b, scale, flags);
+  if (s != BIMAMBA_OK) return s;
+  if (!dout || !dq || !dk || !dv || !ddt || !dA || !db) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const bimamba::delta::Plan p =
+      bimamba::delta::make_bwd_plan(batch, seqlen, nheads_k, nheads, headdim_k, headdim_v);
+  if (workspace_bytes < p.total) return BIMAMBA_ERR_WORKSPACE_TOO_SMALL;
+  if (!workspace) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const size_t rows = static_cast<size_t>(batch) * seqlen;
+  const size_t key = rows * nheads_k * headdim_k * 2, val = rows * nheads * headdim_v * 2, tok = rows * nheads * 2;
+  const size_t st = static_cast<size_t>(batch) * nheads * headdim_k * headdim_v * 4, par = static_cast<size_t>(nheads) * 4;
+  // dh_in may be dh_out itself, as h_out may be h_in in the forward call
+  if (dh_out && !aligned(dh_out, 16)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const Buf bufs[] = {{dq, key, 16}, {dk, key, 16}, {dv, val, 16}, {ddt, tok, 2}, {dA, par, 4}, {db, tok, 2},
+                      {ddt_bias, par, 4}, {dh_in, st, 16}, {workspace, p.total, 256},
+                      {dout, val, 16}, {q, key, 16}, {k, key, 16}, {v, val, 16}, {dt, tok, 2}, {A, par, 4}, {b, tok, 2},
+                      {dt_bias, par, 4}, {h_in, st, 16}, {dh_out == dh_in ? nullptr : dh_out, st, 16}};
+  if (!buffers_ok(bufs, static_cast<int>(sizeof(bufs) / sizeof(bufs[0])), 9)) return BIMAMBA_ERR_INVALID_ARGUMENT;
+  const bimamba::delta::DeltaArgs a{q, k, v, dt, A, b, dt_bias, h_in, nullptr, nullptr, batch, seqlen, nheads_k, nheads,
+                                    headdim_k, headdim_v, scale, (flags & BIMAMBA_FLAG_REV_ONLY) ? 1 : 0};
+  const bimamba::delta::DeltaGrads g{dout, dh_out, dq, dk, dv, ddt, dA, db, ddt_bias, dh_in};
+  return map_hip(bimamba::delta::launch_delta_bwd(a, g, p, workspace, stream));
 }
 
 }  // extern "C"

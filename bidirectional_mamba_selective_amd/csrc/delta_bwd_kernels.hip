@@ -1,0 +1,604 @@
+// Backward pass of the gated delta rule (delta_kernels.hip has the forward pass and its symbols) for gfx950.  With dO the
+// gradient of O, dS that of the state after a chunk, R = V - diag(e^g) K S and all of it per chunk of 64 tokens:
+//   dU = A^T dO + diag(e^(g_C - g)) K dS,   dR = T^T dU = dV
+//   dS_before = e^(g_C) dS + scale (diag(e^g) Q)^T dO - (diag(e^g) K)^T dR
+//   D1_ij = scale e^(g_i - g_j) dO_i.U_j (j <= i),   D2_ij = -e^(g_i - g_j) dR_i.U_j (j < i)
+//   dQ = scale diag(e^g) dO S^T + D1 K
+//   dK = -diag(e^g) dR S^T + D2 K + diag(e^(g_C - g)) U dS^T + D1^T Q + D2^T K
+//   db_i = (1 - beta_i) / beta_i dR_i.U_i        (both factors carry a beta_i)
+// A token's log decay multiplies every term that reaches across it, so its gradient is the sum of just those terms (no
+// sums that cancel): with P_ij = D1_ij q_i.k_j + D2_ij k_i.k_j, s_i = scale e^(g_i) dO_i.S^T q_i - e^(g_i) dR_i.S^T k_i,
+// e_j = e^(g_C - g_j) U_j.dS^T k_j,
+//   dg_t = sum_{j < t <= i} P_ij + sum_{i >= t} s_i + sum_{j < t} e_j + e^(g_C) <S, dS>
+//
+// The chunks' operands and states come from the forward kernels, which run again; k_delta_rwalk goes over the chunks from
+// the last to the first as k_delta_walk goes the other way; k_delta_grads then takes all chunks at once, a workgroup per
+// chunk and key head, so that the gradients of shared keys and queries are summed in registers in a fixed order.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "delta_device.h"
+#include "launch.h"
+
+namespace bimamba {
+namespace delta {
+namespace {
+
+constexpr int C = static_cast<int>(kC);
+
+struct RWalkArgs {
+  const uint16_t* dout;
+  const uint16_t* k;
+  uint16_t* dv_out;
+  const unsigned char* heads;
+  const unsigned char* keys;
+  const float* dh_out;  // null: zeros
+  float* dh_in;         // null: not written
+  float* dstates;       // dS after each chunk, [batch][head][chunk][dk][dv]
+  float* drs;           // dR, [batch][head][chunk][64][dv]
+  Shape sh;
+  Layout lay;
+  int64_t batch, dv, chunks;
+  float scale;
+};
+
+// Heads over XCDs as in the forward walk: the workgroups of one head share an L2.
+__device__ __forceinline__ bool place(int64_t slices, int64_t rows, int64_t* row, int64_t* slice) {
+  const int64_t x = blockIdx.x & 7, i = blockIdx.x >> 3;
+  *row = i / slices * 8 + x;
+  *slice = i % slices;
+  return *row < rows;
+}
+
+template <int DK, int NT>
+__global__ __launch_bounds__(256) void k_delta_rwalk(RWalkArgs a) {
+  constexpr int KS = DK / 32, ST = DK / 64, NS = 16 * NT;
+  __shared__ __align__(16) uint16_t sS[3][NS * DK], sD[NS * C], sE[3][NS * C], sR[3][NS * C], sU[3][NS * C];
+  const int lane = threadIdx.x & 63, l16 = lane & 15, q4 = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int64_t bh, slice;
+  if (!place(a.dv / NS, a.batch * a.sh.heads, &bh, &slice)) return;
+  const int64_t b = bh / a.sh.heads, h = bh % a.sh.heads, kh = h / (a.sh.heads / a.sh.hk);
+  const int64_t L = a.sh.L, n0 = slice * NS;
+  const unsigned char* rec = a.heads + bh * a.chunks * a.lay.bytes;
+  const unsigned char* key = a.keys + (b * a.sh.hk + kh) * a.chunks * a.lay.key_bytes;
+
+  f32x4 S[ST][NT];
+#pragma unroll
+  for (int st = 0; st < ST; ++st)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int64_t i = (bh * DK + 16 * (ST * w + st) + 4 * q4 + r) * a.dv + n0 + 16 * nt + l16;
+        S[st][nt][r] = a.dh_out ? a.dh_out[i] : 0.0f;
+      }
+
+  bf16x8 kf[KS], tf[2][3], af[2][3], ktf[ST][2], qtf[ST][2];
+  uint16_t vv[NT][4];
+  f32x4 eg, keep;
+  float last;
+  auto load_k = [&](int64_t ci) {
+    const int64_t p = ci * C + 16 * w + l16;
+    const uint16_t* row = a.k + ((b * L + a.sh.token(p < L ? p : L - 1)) * a.sh.hk + kh) * DK + 8 * q4;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      kf[s] = *reinterpret_cast<const bf16x8*>(row + 32 * s);
+      if (p >= L) kf[s] = zero8();
+    }
+  };
+  auto load_do = [&](int64_t ci) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int64_t p = ci * C + 16 * w + 4 * q4 + r;
+      const uint16_t* row = a.dout + ((b * L + a.sh.token(p < L ? p : L - 1)) * a.sh.heads + h) * a.dv + n0 + l16;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) vv[nt][r] = p < L ? row[16 * nt] : static_cast<uint16_t>(0);
+    }
+  };
+  auto load_tri = [&](int64_t ci, size_t off, bf16x8(&f)[2][3]) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      if (upper_has(w, s))
+#pragma unroll
+        for (int i = 0; i < 3; ++i) f[s][i] = load_frag(rec + ci * a.lay.bytes + off, upper_at(w, s) * 3 + i, lane);
+  };
+  auto load_keys = [&](int64_t ci) {
+#pragma unroll
+    for (int st = 0; st < ST; ++st)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        ktf[st][s] = load_frag(key + ci * a.lay.key_bytes, (ST * w + st) * 2 + s, lane);
+        qtf[st][s] = load_frag(key + ci * a.lay.key_bytes, DK / 8 + (ST * w + st) * 2 + s, lane);
+      }
+  };
+  auto load_gates = [&](int64_t ci) {
+    const float* g = reinterpret_cast<const float*>(rec + ci * a.lay.bytes);
+    eg = *reinterpret_cast<const f32x4*>(g + 16 * w + 4 * q4);
+    keep = *reinterpret_cast<const f32x4*>(g + C + 16 * w + 4 * q4);
+    last = g[C - 1];
+  };
+  {
+    const int64_t c = a.chunks - 1;
+    load_k(c), load_do(c), load_tri(c, a.lay.tt, tf), load_tri(c, a.lay.at, af), load_keys(c), load_gates(c);
+  }
+
+  for (int64_t ci = a.chunks - 1; ci >= 0; --ci) {
+    const int64_t next = ci > 0 ? ci - 1 : 0;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int st = 0; st < ST; ++st) {
+        u32x2 p[3];
+        split4(S[st][nt], p);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) write4<DK>(sS[i], 16 * nt + l16, 16 * (ST * w + st) + 4 * q4, p[i]);
+        float* to = a.dstates + ((bh * a.chunks + ci) * DK + 16 * (ST * w + st) + 4 * q4) * a.dv + n0 + 16 * nt + l16;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) to[r * a.dv] = S[st][nt][r];
+      }
+      const u32x2 raw = {vv[nt][0] | static_cast<uint32_t>(vv[nt][1]) << 16,
+                         vv[nt][2] | static_cast<uint32_t>(vv[nt][3]) << 16};
+      write4<C>(sD, 16 * nt + l16, 16 * w + 4 * q4, raw);
+      u32x2 p[3];
+      split4(__builtin_convertvector(__builtin_bit_cast(bf16x4, raw), f32x4) * (eg * a.scale), p);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) write4<C>(sE[i], 16 * nt + l16, 16 * w + 4 * q4, p[i]);
+    }
+    load_do(next);
+    __syncthreads();
+    f32x4 U[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      U[nt] = zero4();
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const bf16x8 x[1] = {kf[s]};
+        bf16x8 y[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) y[i] = read8<DK>(sS[i], 16 * nt + l16, 32 * s + 8 * q4);
+        U[nt] = mfma_parts(x, y, U[nt]);
+      }
+      U[nt] *= keep;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (upper_has(w, s)) {
+          const bf16x8 y[1] = {read8<C>(sD, 16 * nt + l16, 32 * s + 8 * q4)};
+          U[nt] = mfma_parts(af[s], y, U[nt]);
+        }
+      u32x2 p[3];
+      split4(U[nt], p);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) write4<C>(sR[i], 16 * nt + l16, 16 * w + 4 * q4, p[i]);
+    }
+    load_k(next), load_tri(next, a.lay.at, af);
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      f32x4 R = zero4();
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (upper_has(w, s)) {
+          bf16x8 y[3];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) y[i] = read8<C>(sR[i], 16 * nt + l16, 32 * s + 8 * q4);
+          R = mfma_parts(tf[s], y, R);
+        }
+      u32x2 p[3];
+      split4(-eg * R, p);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) write4<C>(sU[i], 16 * nt + l16, 16 * w + 4 * q4, p[i]);
+      float* to = a.drs + ((bh * a.chunks + ci) * C + 16 * w + 4 * q4) * a.dv + n0 + 16 * nt + l16;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        to[r * a.dv] = R[r];
+        const int64_t t = ci * C + 16 * w + 4 * q4 + r;
+        if (t < L) {
+          bf16_t o;
+          from_f32(R[r], &o);
+          a.dv_out[((b * L + a.sh.token(t)) * a.sh.heads + h) * a.dv + n0 + 16 * nt + l16] = o.bits;
+        }
+      }
+    }
+    load_tri(next, a.lay.tt, tf);
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int st = 0; st < ST; ++st) S[st][nt] *= last;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        bf16x8 y[3], z[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          y[i] = read8<C>(sU[i], 16 * nt + l16, 32 * s + 8 * q4);
+          z[i] = read8<C>(sE[i], 16 * nt + l16, 32 * s + 8 * q4);
+        }
+#pragma unroll
+        for (int st = 0; st < ST; ++st) {
+          const bf16x8 x[1] = {ktf[st][s]}, u[1] = {qtf[st][s]};
+          S[st][nt] = mfma_parts(x, y, S[st][nt]);
+          S[st][nt] = mfma_parts(u, z, S[st][nt]);
+        }
+      }
+    }
+    load_keys(next), load_gates(next);
+    // sE and sD are written again before the next barrier
+    __syncthreads();
+  }
+  if (a.dh_in) {
+#pragma unroll
+    for (int st = 0; st < ST; ++st)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          a.dh_in[(bh * DK + 16 * (ST * w + st) + 4 * q4 + r) * a.dv + n0 + 16 * nt + l16] = S[st][nt][r];
+  }
+}
+
+struct GradArgs {
+  const uint16_t* dout;
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* dt;
+  const uint16_t* b;
+  const float* A;
+  const float* dt_bias;
+  uint16_t* dq;
+  uint16_t* dk;
+  uint16_t* ddt;
+  uint16_t* db;
+  const unsigned char* heads;
+  const unsigned char* keys;
+  const float* states;
+  const float* dstates;
+  const float* us;
+  const float* drs;
+  float* part;  // [batch][head][chunk][2]: the chunk's sums for dA and ddt_bias
+  Shape sh;
+  Layout lay;
+  int64_t chunks;
+  float scale;
+};
+
+__device__ __forceinline__ f32x8 load_f32x8(const float* p) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+  return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+
+// Sum over the 16 lanes of a row.
+__device__ __forceinline__ float sum16(float v) {
+  v = add_dpp<0xB1>(v);
+  v = add_dpp<0x4E>(v);
+  v = add_dpp<0x141>(v);
+  return add_dpp<0x140>(v);
+}
+
+// Sum over lanes l, l ^ 16, l ^ 32, l ^ 48.
+__device__ __forceinline__ float sum_rows(float v) {
+  auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+
+template <int DK, int DV>
+__global__ __launch_bounds__(256) void k_delta_grads(GradArgs a) {
+  constexpr int KS = DK / 32, VS = DV / 32, KT = DK / 16, kRow = DK + 8, kPitch = C + 1;
+  __shared__ __align__(16) uint16_t sD1[2][C * C], sD1t[2][C * C], sD2[2][C * C], sD2t[2][C * C];
+  __shared__ __align__(16) uint16_t sQ[C * kRow], sK[C * kRow];
+  __shared__ float sP[C * kPitch];
+  __shared__ float sHi[C], sLo[C], sEg[C], sKeep[C], sS0[C], sS1[C], sDb[C], sAcc[4][C], sDot[4];
+  const int lane = threadIdx.x & 63, l16 = lane & 15, q4 = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t ci = blockIdx.x, kh = blockIdx.y, b = blockIdx.z, L = a.sh.L, share = a.sh.heads / a.sh.hk;
+  const int64_t p0 = ci * C;
+  const unsigned char* key = a.keys + ((b * a.sh.hk + kh) * a.chunks + ci) * a.lay.key_bytes;
+
+  bf16x8 kf[KS], qf[KS];
+  {
+    const int64_t p = p0 + 16 * w + l16;
+    const int64_t row = ((b * L + a.sh.token(p < L ? p : L - 1)) * a.sh.hk + kh) * DK + 8 * q4;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      kf[s] = *reinterpret_cast<const bf16x8*>(a.k + row + 32 * s);
+      qf[s] = *reinterpret_cast<const bf16x8*>(a.q + row + 32 * s);
+      if (p >= L) kf[s] = qf[s] = zero8();
+      *reinterpret_cast<bf16x8*>(sK + (16 * w + l16) * kRow + 32 * s + 8 * q4) = kf[s];
+      *reinterpret_cast<bf16x8*>(sQ + (16 * w + l16) * kRow + 32 * s + 8 * q4) = qf[s];
+    }
+  }
+  f32x4 dq[KT], dk[KT];
+#pragma unroll
+  for (int i = 0; i < KT; ++i) dq[i] = dk[i] = zero4();
+
+  for (int64_t g = 0; g < share; ++g) {
+    const int64_t h = kh * share + g, bh = b * a.sh.heads + h, hc = bh * a.chunks + ci;
+    const float* gates = reinterpret_cast<const float*>(a.heads + hc * a.lay.bytes);
+    __syncthreads();  // the previous head's readers of what is written here
+    if (w == 0) sEg[lane] = gates[lane], sKeep[lane] = gates[C + lane];
+    if (w == 1) sHi[lane] = gates[2 * C + lane], sLo[lane] = gates[3 * C + lane];
+    // this wavefront's rows of dO, dR and U as operands
+    bf16x8 od[VS], rd[VS][2], ud[VS][2];
+    {
+      const int64_t p = p0 + 16 * w + l16;
+      const uint16_t* row = a.dout + ((b * L + a.sh.token(p < L ? p : L - 1)) * a.sh.heads + h) * DV + 8 * q4;
+      float dot = 0.0f;
+      const float beta = gates[4 * C + 16 * w + l16];
+      const float rb = beta > 1e-30f ? 1.0f / beta : 0.0f;
+#pragma unroll
+      for (int s = 0; s < VS; ++s) {
+        od[s] = *reinterpret_cast<const bf16x8*>(row + 32 * s);
+        if (p >= L) od[s] = zero8();
+        const f32x8 r = load_f32x8(a.drs + (hc * C + 16 * w + l16) * DV + 32 * s + 8 * q4);
+        const f32x8 u = load_f32x8(a.us + (hc * C + 16 * w + l16) * DV + 32 * s + 8 * q4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dot = fmaf(u[e] * rb, r[e], dot);
+        split8(r, rd[s]);
+        split8(u, ud[s]);
+      }
+      dot = sum_rows(dot);
+      if (q4 == 0) sDb[16 * w + l16] = dot;
+    }
+    __syncthreads();
+    const f32x4 eg = *reinterpret_cast<const f32x4*>(sEg + 16 * w + 4 * q4);
+    const f32x4 keep = *reinterpret_cast<const f32x4*>(sKeep + 16 * w + 4 * q4);
+
+    for (int j = 0; j < 4; ++j) {
+      f32x4 d1 = zero4(), d2 = zero4(), pr = zero4();
+      if (j <= w) {
+        f32x4 qk = zero4(), kk = zero4();
+#pragma unroll
+        for (int s = 0; s < VS; ++s) {
+          bf16x8 u[2];
+          split8(load_f32x8(a.us + (hc * C + 16 * j + l16) * DV + 32 * s + 8 * q4), u);
+          const bf16x8 x[1] = {od[s]};
+          d1 = mfma_parts(x, u, d1);
+          d2 = mfma_parts(rd[s], u, d2);
+        }
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const bf16x8 o = *reinterpret_cast<const bf16x8*>(sK + (16 * j + l16) * kRow + 32 * s + 8 * q4);
+          qk = mfma(qf[s], o, qk);
+          kk = mfma(kf[s], o, kk);
+        }
+        const int col = 16 * j + l16;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * w + 4 * q4 + r;
+          const float d = col <= row ? ex((sHi[row] - sHi[col]) + (sLo[row] - sLo[col])) : 0.0f;
+          d1[r] = col <= row ? d1[r] * d * a.scale : 0.0f;
+          d2[r] = col < row ? -d2[r] * d : 0.0f;
+          pr[r] = col < row ? fmaf(d1[r], qk[r], d2[r] * kk[r]) : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sP[(16 * w + 4 * q4 + r) * kPitch + 16 * j + l16] = pr[r];
+      u32x2 p1[2], p2[2];
+      split4(d1, p1);
+      split4(d2, p2);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        write4<C>(sD1t[i], 16 * j + l16, 16 * w + 4 * q4, p1[i]);
+        write4<C>(sD2t[i], 16 * j + l16, 16 * w + 4 * q4, p2[i]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          sD1[i][at<C>(16 * w + 4 * q4 + r, 16 * j + l16)] = static_cast<uint16_t>(p1[i][r >> 1] >> (16 * (r & 1)));
+          sD2[i][at<C>(16 * w + 4 * q4 + r, 16 * j + l16)] = static_cast<uint16_t>(p2[i][r >> 1] >> (16 * (r & 1)));
+        }
+      }
+    }
+    // products with the states
+    f32x4 s0 = zero4(), s1 = zero4();
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < KT; ++i) {
+      f32x4 t1 = zero4(), t2 = zero4(), t3 = zero4();
+#pragma unroll
+      for (int s = 0; s < VS; ++s) {
+        const int64_t at_row = (hc * DK + 16 * i + l16) * DV + 32 * s + 8 * q4;
+        const f32x8 st = load_f32x8(a.states + at_row), ds = load_f32x8(a.dstates + at_row);
+        if ((i & 3) == w) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dot = fmaf(st[e], ds[e], dot);
+        }
+        bf16x8 y[2], z[2];
+        split8(st, y);
+        split8(ds, z);
+        const bf16x8 x[1] = {od[s]};
+        t1 = mfma_parts(x, y, t1);
+        t2 = mfma_parts(rd[s], y, t2);
+        t3 = mfma_parts(ud[s], z, t3);
+      }
+      t1 *= eg * a.scale;
+      t2 *= -eg;
+      t3 *= keep;
+      dq[i] += t1;
+      dk[i] += t2 + t3;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int e = (16 * w + 4 * q4 + r) * kRow + 16 * i + l16;
+        const float kv = bf(sK[e]);
+        s0[r] = fmaf(bf(sQ[e]), t1[r], fmaf(kv, t2[r], s0[r]));
+        s1[r] = fmaf(kv, t3[r], s1[r]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float v0 = sum16(s0[r]), v1 = sum16(s1[r]);
+      if (l16 == 0) sS0[16 * w + 4 * q4 + r] = v0, sS1[16 * w + 4 * q4 + r] = v1;
+    }
+    dot = sum_rows(sum16(dot));
+    if (lane == 0) sDot[w] = dot;
+    __syncthreads();
+
+    // products within the chunk
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      bf16x8 d1[2], d2[2], d1t[2], d2t[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        d1[i] = read8<C>(sD1[i], 16 * w + l16, 32 * s + 8 * q4);
+        d2[i] = read8<C>(sD2[i], 16 * w + l16, 32 * s + 8 * q4);
+        d1t[i] = read8<C>(sD1t[i], 16 * w + l16, 32 * s + 8 * q4);
+        d2t[i] = read8<C>(sD2t[i], 16 * w + l16, 32 * s + 8 * q4);
+      }
+#pragma unroll
+      for (int i = 0; i < KT; ++i) {
+        const bf16x8 kt[1] = {load_frag(key, 2 * i + s, lane)};
+        if (lower_has(w, s)) {
+          dq[i] = mfma_parts(d1, kt, dq[i]);
+          dk[i] = mfma_parts(d2, kt, dk[i]);
+        }
+        if (upper_has(w, s)) {
+          const bf16x8 qt[1] = {load_frag(key, DK / 8 + 2 * i + s, lane)};
+          dk[i] = mfma_parts(d1t, qt, dk[i]);
+          dk[i] = mfma_parts(d2t, kt, dk[i]);
+        }
+      }
+    }
+    // sum of P_ij over j < t <= i: prefix sums along 16 rows of each wavefront, added for the rows from t on
+    {
+      float acc = 0.0f;
+#pragma unroll 4
+      for (int r = 0; r < 16; ++r) {
+        const int i = 16 * w + r;
+        float v = sP[i * kPitch + lane];
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+          const float up = __shfl_up(v, d);
+          if (lane >= d) v += up;
+        }
+        const float before = __shfl_up(v, 1);
+        if (lane > 0 && i >= lane) acc += before;
+      }
+      sAcc[w][lane] = acc;
+    }
+    __syncthreads();
+    if (w == 0) {
+      // sums of s over i >= t and of e over j < t
+      float v0 = sS0[lane], v1 = sS1[lane];
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const float down = __shfl_down(v0, d), up = __shfl_up(v1, d);
+        if (lane + d < 64) v0 += down;
+        if (lane >= d) v1 += up;
+      }
+      const float before = __shfl_up(v1, 1);
+      const float last = sEg[C - 1];
+      float dg = ((sAcc[0][lane] + sAcc[1][lane]) + (sAcc[2][lane] + sAcc[3][lane])) + v0 + (lane > 0 ? before : 0.0f);
+      dg = fmaf(last, (sDot[0] + sDot[1]) + (sDot[2] + sDot[3]), dg);
+      const int64_t p = p0 + lane;
+      float pa = 0.0f, pb = 0.0f;
+      if (p < L) {
+        const int64_t t = (b * L + a.sh.token(p)) * a.sh.heads + h;
+        const float x = bf(a.dt[t]) + (a.dt_bias ? a.dt_bias[h] : 0.0f);
+        const float ddt = dg * a.A[h] * sigmoid_f32(x);
+        pa = dg * softplus_f32(x);
+        pb = ddt;
+        bf16_t o;
+        from_f32(ddt, &o);
+        a.ddt[t] = o.bits;
+        from_f32(sDb[lane] * sigmoid_f32(-bf(a.b[t])), &o);
+        a.db[t] = o.bits;
+      }
+      pa = sum_rows(sum16(pa));
+      pb = sum_rows(sum16(pb));
+      if (lane == 0) a.part[2 * hc] = pa, a.part[2 * hc + 1] = pb;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < KT; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int64_t p = p0 + 16 * w + 4 * q4 + r;
+      if (p < L) {
+        const int64_t to = ((b * L + a.sh.token(p)) * a.sh.hk + kh) * DK + 16 * i + l16;
+        bf16_t o;
+        from_f32(dq[i][r], &o);
+        a.dq[to] = o.bits;
+        from_f32(dk[i][r], &o);
+        a.dk[to] = o.bits;
+      }
+    }
+}
+
+// dA and ddt_bias of one head: its chunks' sums over all batch elements, in a fixed order.
+__global__ __launch_bounds__(256) void k_delta_reduce(const float* part, float* dA, float* ddt_bias, int64_t batch,
+                                                      int64_t heads, int64_t chunks) {
+  __shared__ float s[2][4];
+  const int64_t h = blockIdx.x;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  float x = 0.0f, y = 0.0f;
+  for (int64_t b = 0; b < batch; ++b) {
+    const float* p = part + (b * heads + h) * chunks * 2;
+    for (int64_t c = threadIdx.x; c < chunks; c += 256) x += p[2 * c], y += p[2 * c + 1];
+  }
+  x = sum_rows(sum16(x));
+  y = sum_rows(sum16(y));
+  if (lane == 0) s[0][w] = x, s[1][w] = y;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  dA[h] = (s[0][0] + s[0][1]) + (s[0][2] + s[0][3]);
+  if (ddt_bias) ddt_bias[h] = (s[1][0] + s[1][1]) + (s[1][2] + s[1][3]);
+}
+
+template <int DK>
+void launch_rwalk(const RWalkArgs& a, int tiles, hipStream_t stream) {
+  const int64_t rows = (a.batch * a.sh.heads + 7) / 8 * 8;
+  const dim3 grid(static_cast<unsigned>(rows * (a.dv / (16 * tiles))));
+  if (tiles == 1) hipLaunchKernelGGL((k_delta_rwalk<DK, 1>), grid, dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((k_delta_rwalk<DK, 2>), grid, dim3(256), 0, stream, a);
+}
+
+template <int DK>
+void launch_grads(const GradArgs& a, int64_t dv, dim3 grid, hipStream_t stream) {
+  if (dv == 64) hipLaunchKernelGGL((k_delta_grads<DK, 64>), grid, dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((k_delta_grads<DK, 128>), grid, dim3(256), 0, stream, a);
+}
+
+}  // namespace
+
+hipError_t launch_delta_bwd(const DeltaArgs& in, const DeltaGrads& g, const Plan& p, void* ws, hipStream_t stream) {
+  unsigned char* base = static_cast<unsigned char*>(ws);
+  const Layout lay = make_layout(in.dk, true);
+  const Shape sh{in.seqlen, in.hk, in.heads, in.rev};
+  float* states = reinterpret_cast<float*>(base + p.s_off);
+  float* dstates = reinterpret_cast<float*>(base + p.ds_off);
+  float* us = reinterpret_cast<float*>(base + p.u_off);
+  float* drs = reinterpret_cast<float*>(base + p.dr_off);
+  float* part = reinterpret_cast<float*>(base + p.part_off);
+  hipError_t e = launch_delta_prep(in, p, 0, p.nchunk, true, ws, stream);
+  if (e != hipSuccess) return e;
+  e = launch_delta_walk(in, p, 0, p.nchunk, true, in.h_in, nullptr, ws, stream);
+  if (e != hipSuccess) return e;
+  const uint16_t* dout = static_cast<const uint16_t*>(g.dout);
+  const uint16_t* k = static_cast<const uint16_t*>(in.k);
+  const RWalkArgs r{dout, k, static_cast<uint16_t*>(g.dv), base + p.head_off, base + p.key_off, g.dh_out, g.dh_in,
+                    dstates, drs, sh, lay, in.batch, in.dv, p.nchunk, in.scale};
+  if (in.dk == 64) launch_rwalk<64>(r, p.tiles, stream);
+  else launch_rwalk<128>(r, p.tiles, stream);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const GradArgs a{dout, static_cast<const uint16_t*>(in.q), k, static_cast<const uint16_t*>(in.dt),
+                   static_cast<const uint16_t*>(in.b), in.A, in.dt_bias, static_cast<uint16_t*>(g.dq),
+                   static_cast<uint16_t*>(g.dk), static_cast<uint16_t*>(g.ddt), static_cast<uint16_t*>(g.db),
+                   base + p.head_off, base + p.key_off, states, dstates, us, drs, part, sh, lay, p.nchunk, in.scale};
+  const dim3 grid(static_cast<unsigned>(p.nchunk), static_cast<unsigned>(in.hk), static_cast<unsigned>(in.batch));
+  if (in.dk == 64) launch_grads<64>(a, in.dv, grid, stream);
+  else launch_grads<128>(a, in.dv, grid, stream);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_delta_reduce, dim3(static_cast<unsigned>(in.heads)), dim3(256), 0, stream, part, g.dA,
+                     g.ddt_bias, in.batch, in.heads, p.nchunk);
+  return hipGetLastError();
+}
+
+}  // namespace delta
+}  // namespace bimamba

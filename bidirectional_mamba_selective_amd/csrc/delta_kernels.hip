@@ -1,0 +1,647 @@
+// The gated delta rule for gfx950: a recurrent mixer whose state is a dk x dv matrix per head,
+//   delta = softplus(dt + dt_bias), a = exp(delta A), beta = sigmoid(b)
+//   S_t = a_t S_{t-1} + beta_t k_t (v_t - (a_t S_{t-1})^T k_t)^T,     o_t = scale S_t^T q_t
+// over chunks of 64 tokens.  With g the logarithms of the decays summed from the chunk's start, S the state that enters,
+// N_ij = beta_i e^(g_i - g_j) k_i.k_j (j < i) and A_ij = scale e^(g_i - g_j) q_i.k_j (j <= i), the corrections u_t that
+// the tokens add to the state solve a unit lower triangular system:
+//   U = T (V - diag(e^g) K S),  T = (I + N)^-1 diag(beta)
+//   O = scale diag(e^g) Q S + A U,     S' = e^(g_C) S + K^T diag(e^(g_C - g)) U
+// Every decay is exp of a difference g_i - g_j <= 0, never a quotient, so strong decays neither overflow nor divide by
+// zero.
+//
+// k_delta_prep forms T, A, the decays and K^T of all chunks at once; k_delta_walk then goes over the chunks with the state
+// in fp32 registers, a workgroup per head and 16 or 32 columns of it (the columns of S, U, V and O are independent).
+// Products run on the matrix cores with bf16 operands and fp32 sums.  q, k and v are bf16 already; S, U and T are taken
+// as three bf16 parts (24 bits), so a state keeps fp32 accuracy over any number of chunks; A and the copies of S and U
+// that only the bf16 output sees, as two.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "delta_device.h"
+#include "launch.h"
+
+namespace bimamba {
+namespace delta {
+namespace {
+
+constexpr int C = static_cast<int>(kC);
+constexpr int kPitch = C + 1;  // fp32 rows in LDS
+
+struct PrepArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* dt;
+  const uint16_t* b;
+  const float* A;
+  const float* dt_bias;
+  unsigned char* heads;  // records of Layout::bytes, [batch][head][seg]
+  unsigned char* keys;   // K^T (and Q^T), [batch][key head][seg]
+  Shape sh;
+  Layout lay;
+  int64_t chunk0, seg;  // first chunk of the segment, records per head
+  float scale;
+};
+
+__device__ __forceinline__ void put_tile(float* s, int row0, int col0, int l16, int q4, f32x4 v) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) s[(row0 + 4 * q4 + r) * kPitch + col0 + l16] = v[r];
+}
+
+// sum over K of X[row0 + ., k0 + .] Y[k1 + ., col0 + .], 16 x 16 results, KT x 16 terms, from fp32 rows in LDS.
+template <int KT>
+__device__ __forceinline__ f32x4 tile_product(const float* x, int row0, int k0, const float* y, int k1, int col0,
+                                              int l16, int q4) {
+  f32x4 acc = zero4();
+#pragma unroll
+  for (int s = 0; s < 4 * KT; ++s)
+    acc = mfma_f32(x[(row0 + l16) * kPitch + k0 + 4 * s + q4], y[(k1 + 4 * s + q4) * kPitch + col0 + l16], acc);
+  return acc;
+}
+
+// One workgroup per (chunk, head, batch element).  The record's gates: e^g, e^(g_C - g), g as two floats whose sum carries
+// it to 2^-48 (differences of g stay exact to fp32 however far the chunk has decayed), beta; 64 of each.
+template <int DK, bool GRAD>
+__global__ __launch_bounds__(256) void k_delta_prep(PrepArgs a) {
+  constexpr int KS = DK / 32;
+  constexpr int kRow = DK + 8;
+  __shared__ float sN[C * kPitch], sT[C * kPitch], sA[C * kPitch];
+  __shared__ float sHi[C], sLo[C], sBeta[C];
+  __shared__ uint16_t sK[C * kRow];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, l16 = lane & 15, q4 = lane >> 4;
+  const int64_t ci = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const int64_t share = a.sh.heads / a.sh.hk, kh = h / share, L = a.sh.L;
+  const int64_t p0 = (a.chunk0 + ci) * C;
+  unsigned char* rec = a.heads + ((b * a.sh.heads + h) * a.seg + ci) * a.lay.bytes;
+  float* gates = reinterpret_cast<float*>(rec);
+
+  // tokens past the end: q = k = 0, no decay, beta = 0; they change nothing
+  if (w == 0) {
+    const int64_t p = p0 + lane;
+    float g = 0.0f, beta = 0.0f;
+    if (p < L) {
+      const int64_t i = (b * L + a.sh.token(p)) * a.sh.heads + h;
+      g = softplus_f32(bf(a.dt[i]) + (a.dt_bias ? a.dt_bias[h] : 0.0f)) * a.A[h];
+      // e^-256 is 0 in fp32 as any stronger decay is; sums of the logarithms stay finite
+      if (g < -256.0f) g = -256.0f;
+      beta = sigmoid_f32(bf(a.b[i]));
+    }
+    double sum = g;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const double up = __shfl_up(sum, d);
+      if (lane >= d) sum += up;
+    }
+    const double end = __shfl(sum, 63);
+    const float hi = static_cast<float>(sum);
+    const float lo = static_cast<float>(sum - static_cast<double>(hi));
+    sHi[lane] = hi, sLo[lane] = lo, sBeta[lane] = beta;
+    gates[lane] = ex(hi);
+    gates[C + lane] = ex(static_cast<float>(end - sum));
+    gates[2 * C + lane] = hi;
+    gates[3 * C + lane] = lo;
+    gates[4 * C + lane] = beta;
+  }
+  bf16x8 kf[KS], qf[KS];
+  {
+    const int64_t p = p0 + 16 * w + l16;
+    const int64_t row = ((b * L + a.sh.token(p < L ? p : L - 1)) * a.sh.hk + kh) * DK;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      kf[s] = *reinterpret_cast<const bf16x8*>(a.k + row + 32 * s + 8 * q4);
+      qf[s] = *reinterpret_cast<const bf16x8*>(a.q + row + 32 * s + 8 * q4);
+      if (p >= L) kf[s] = qf[s] = zero8();
+      *reinterpret_cast<bf16x8*>(sK + (16 * w + l16) * kRow + 32 * s + 8 * q4) = kf[s];
+    }
+  }
+  __syncthreads();
+
+  // scores of this wavefront's 16 rows against the tokens up to them
+  for (int j = 0; j <= w; ++j) {
+    f32x4 kk = zero4(), qk = zero4();
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const bf16x8 o = *reinterpret_cast<const bf16x8*>(sK + (16 * j + l16) * kRow + 32 * s + 8 * q4);
+      kk = mfma(kf[s], o, kk);
+      qk = mfma(qf[s], o, qk);
+    }
+    const int col = 16 * j + l16;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * w + 4 * q4 + r;
+      const float d = col <= row ? ex((sHi[row] - sHi[col]) + (sLo[row] - sLo[col])) : 0.0f;
+      kk[r] = col < row ? kk[r] * d * sBeta[row] : 0.0f;
+      qk[r] = col <= row ? qk[r] * d * a.scale : 0.0f;
+    }
+    put_tile(sN, 16 * w, 16 * j, l16, q4, kk);
+    put_tile(sA, 16 * w, 16 * j, l16, q4, qk);
+  }
+  __syncthreads();
+
+  // (I + N)^-1: the four 16 x 16 blocks on the diagonal by substitution, a column per lane, then blocks joined two by
+  // two, [[x, 0], [n, y]]^-1 = [[x', 0], [-y' n x', y']], as stable as the substitution.  What is above the diagonal of
+  // sT is scratch.
+  if (w == 0) {
+    const int o = 16 * q4;
+    float t[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float v = i == l16 ? 1.0f : 0.0f;
+#pragma unroll
+      for (int j = 0; j < i; ++j) v = fmaf(-sN[(o + i) * kPitch + o + j], t[j], v);
+      t[i] = v;
+      sT[(o + i) * kPitch + o + l16] = v;
+    }
+  }
+  __syncthreads();
+  if (w < 2) put_tile(sT, 32 * w, 32 * w + 16, l16, q4, tile_product<1>(sN, 32 * w + 16, 32 * w, sT, 32 * w, 32 * w, l16, q4));
+  __syncthreads();
+  if (w < 2)
+    put_tile(sT, 32 * w + 16, 32 * w, l16, q4,
+             -tile_product<1>(sT, 32 * w + 16, 32 * w + 16, sT, 32 * w, 32 * w + 16, l16, q4));
+  __syncthreads();
+  // the upper right block of each half is scratch until now and zero from here on, for the products over 32 terms
+  if (w < 2) put_tile(sT, 32 * w, 32 * w + 16, l16, q4, zero4());
+  __syncthreads();
+  {
+    const int wr = 16 * (w >> 1), wc = 16 * (w & 1);
+    const f32x4 x = tile_product<2>(sN, 32 + wr, 0, sT, 0, wc, l16, q4);
+    put_tile(sT, wr, 32 + wc, l16, q4, x);
+    __syncthreads();
+    const f32x4 y = tile_product<2>(sT, 32 + wr, 32, sT, 0, 32 + wc, l16, q4);
+    put_tile(sT, 32 + wr, wc, l16, q4, -y);
+  }
+  __syncthreads();
+
+  // operands of the walk
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    if (lower_has(w, s)) {
+      const int row = 16 * w + l16;
+      f32x8 t, m;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int col = 32 * s + 8 * q4 + e;
+        t[e] = col <= row ? sT[row * kPitch + col] * sBeta[col] : 0.0f;
+        m[e] = col <= row ? sA[row * kPitch + col] : 0.0f;
+      }
+      bf16x8 tp[3];
+      split8(t, tp);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) store_frag(rec + a.lay.t, lower_at(w, s) * 3 + i, lane, tp[i]);
+      if constexpr (!GRAD) {
+        bf16x8 mp[2];
+        split8(m, mp);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) store_frag(rec + a.lay.a, lower_at(w, s) * 2 + i, lane, mp[i]);
+      }
+    }
+    if constexpr (GRAD) {
+      if (upper_has(w, s)) {
+        const int row = 16 * w + l16;  // the row of the transpose
+        f32x8 t, m;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int col = 32 * s + 8 * q4 + e;
+          t[e] = col >= row ? sT[col * kPitch + row] * sBeta[row] : 0.0f;
+          m[e] = col >= row ? sA[col * kPitch + row] : 0.0f;
+        }
+        bf16x8 tp[3], mp[3];
+        split8(t, tp);
+        split8(m, mp);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          store_frag(rec + a.lay.tt, upper_at(w, s) * 3 + i, lane, tp[i]);
+          store_frag(rec + a.lay.at, upper_at(w, s) * 3 + i, lane, mp[i]);
+        }
+      }
+    }
+  }
+
+  // K^T and Q^T once for the heads that share them
+  if (h % share != 0) return;
+  unsigned char* key = a.keys + ((b * a.sh.hk + kh) * a.seg + ci) * a.lay.key_bytes;
+#pragma unroll
+  for (int which = 0; which < (GRAD ? 2 : 1); ++which) {
+    if (which == 1) {
+      __syncthreads();
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+        *reinterpret_cast<bf16x8*>(sK + (16 * w + l16) * kRow + 32 * s + 8 * q4) = qf[s];
+      __syncthreads();
+    }
+    for (int f = w; f < DK / 8; f += 4) {  // rows 16 (f / 2) of the transpose, tokens 32 (f % 2)
+      union {
+        uint16_t u[8];
+        bf16x8 v;
+      } x;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x.u[e] = sK[(32 * (f & 1) + 8 * q4 + e) * kRow + 16 * (f >> 1) + l16];
+      store_frag(key, which * (DK / 8) + f, lane, x.v);
+    }
+  }
+}
+
+struct WalkArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* out;
+  const unsigned char* heads;
+  const unsigned char* keys;
+  const float* state_in;  // null: zeros
+  float* state_out;       // null: not kept
+  float* states;          // backward: the state entering each chunk, [batch][head][chunk][dk][dv]
+  float* us;              // backward: U, [batch][head][chunk][64][dv]
+  Shape sh;
+  Layout lay;
+  int64_t batch, dv, chunk0, chunks, seg;
+  float scale;
+};
+
+// Workgroups of one head on one XCD, so that what they share is fetched into its L2 once: consecutive workgroups go to
+// the eight XCDs in turn, so head 8 i + x takes the places x, x + 8, ... of the i-th run of 8 x slices workgroups.
+__device__ __forceinline__ bool place(int64_t slices, int64_t rows, int64_t* row, int64_t* slice) {
+  const int64_t x = blockIdx.x & 7, i = blockIdx.x >> 3;
+  *row = i / slices * 8 + x;
+  *slice = i % slices;
+  return *row < rows;
+}
+
+// One workgroup: 16 NT columns of one head's state over `chunks` chunks.  Wavefront w owns the chunk's tokens 16 w .. + 15
+// and a quarter of the state's rows.  Per chunk three products follow from one another (K S, T R, K^T U), each through LDS
+// for the next one's operand, with one barrier before each.  The next chunk's operands are loaded into the registers of the current
+// chunk's as soon as these have been used.
+template <int DK, int NT, bool SAVE>
+__global__ __launch_bounds__(256) void k_delta_walk(WalkArgs a) {
+  constexpr int KS = DK / 32, ST = DK / 64, NS = 16 * NT;
+  __shared__ __align__(16) uint16_t sS[3][NS * DK], sR[3][NS * C], sU[3][NS * C], sV[2][NS * C];
+  const int lane = threadIdx.x & 63, l16 = lane & 15, q4 = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int64_t bh, slice;
+  if (!place(a.dv / NS, a.batch * a.sh.heads, &bh, &slice)) return;
+  const int64_t b = bh / a.sh.heads, h = bh % a.sh.heads, kh = h / (a.sh.heads / a.sh.hk);
+  const int64_t L = a.sh.L, n0 = slice * NS;
+  const unsigned char* rec = a.heads + bh * a.seg * a.lay.bytes;
+  const unsigned char* key = a.keys + (b * a.sh.hk + kh) * a.seg * a.lay.key_bytes;
+
+  f32x4 S[ST][NT];
+#pragma unroll
+  for (int st = 0; st < ST; ++st)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int64_t i = (bh * DK + 16 * (ST * w + st) + 4 * q4 + r) * a.dv + n0 + 16 * nt + l16;
+        S[st][nt][r] = a.state_in ? a.state_in[i] : 0.0f;
+      }
+
+  bf16x8 kf[KS], qf[KS], tf[2][3], af[2][2], ktf[ST][2];
+  uint16_t vv[NT][4];
+  f32x4 eg, keep;
+  float last;
+  auto load_rows = [&](int64_t ci, const uint16_t* src, bf16x8(&f)[KS]) {
+    const int64_t p = (a.chunk0 + ci) * C + 16 * w + l16;
+    const uint16_t* row = src + ((b * L + a.sh.token(p < L ? p : L - 1)) * a.sh.hk + kh) * DK + 8 * q4;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      f[s] = *reinterpret_cast<const bf16x8*>(row + 32 * s);
+      if (p >= L) f[s] = zero8();
+    }
+  };
+  auto load_v = [&](int64_t ci) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int64_t p = (a.chunk0 + ci) * C + 16 * w + 4 * q4 + r;
+      const uint16_t* row = a.v + ((b * L + a.sh.token(p < L ? p : L - 1)) * a.sh.heads + h) * a.dv + n0 + l16;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) vv[nt][r] = p < L ? row[16 * nt] : static_cast<uint16_t>(0);
+    }
+  };
+  auto load_t = [&](int64_t ci) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      if (lower_has(w, s))
+#pragma unroll
+        for (int i = 0; i < 3; ++i) tf[s][i] = load_frag(rec + ci * a.lay.bytes + a.lay.t, lower_at(w, s) * 3 + i, lane);
+  };
+  auto load_a = [&](int64_t ci) {
+    if constexpr (!SAVE) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (lower_has(w, s))
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            af[s][i] = load_frag(rec + ci * a.lay.bytes + a.lay.a, lower_at(w, s) * 2 + i, lane);
+    }
+  };
+  auto load_kt = [&](int64_t ci) {
+#pragma unroll
+    for (int st = 0; st < ST; ++st)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) ktf[st][s] = load_frag(key + ci * a.lay.key_bytes, (ST * w + st) * 2 + s, lane);
+  };
+  auto load_gates = [&](int64_t ci) {
+    const float* g = reinterpret_cast<const float*>(rec + ci * a.lay.bytes);
+    eg = *reinterpret_cast<const f32x4*>(g + 16 * w + 4 * q4);
+    keep = *reinterpret_cast<const f32x4*>(g + C + 16 * w + 4 * q4);
+    last = g[C - 1];
+  };
+  load_rows(0, a.k, kf);
+  if constexpr (!SAVE) load_rows(0, a.q, qf);
+  load_v(0), load_t(0), load_a(0), load_kt(0), load_gates(0);
+
+  for (int64_t ci = 0; ci < a.chunks; ++ci) {
+    const int64_t next = ci + 1 < a.chunks ? ci + 1 : ci;
+#pragma unroll
+    for (int st = 0; st < ST; ++st)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        u32x2 p[3];
+        split4(S[st][nt], p);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) write4<DK>(sS[i], 16 * nt + l16, 16 * (ST * w + st) + 4 * q4, p[i]);
+        if constexpr (SAVE) {
+          float* to = a.states + ((bh * a.seg + ci) * DK + 16 * (ST * w + st) + 4 * q4) * a.dv + n0 + 16 * nt + l16;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) to[r * a.dv] = S[st][nt][r];
+        }
+      }
+    __syncthreads();
+    f32x4 P[NT], O[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      P[nt] = O[nt] = zero4();
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const bf16x8 x[1] = {kf[s]};
+        bf16x8 y[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) y[i] = read8<DK>(sS[i], 16 * nt + l16, 32 * s + 8 * q4);
+        P[nt] = mfma_parts(x, y, P[nt]);
+        if constexpr (!SAVE) {
+          O[nt] = mfma(qf[s], y[1], O[nt]);
+          O[nt] = mfma(qf[s], y[0], O[nt]);
+        }
+      }
+    }
+    load_rows(next, a.k, kf);
+    if constexpr (!SAVE) load_rows(next, a.q, qf);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      f32x4 R;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) R[r] = fmaf(-eg[r], P[nt][r], bf(vv[nt][r]));
+      u32x2 p[3];
+      split4(R, p);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) write4<C>(sR[i], 16 * nt + l16, 16 * w + 4 * q4, p[i]);
+    }
+    load_v(next);
+    __syncthreads();
+    f32x4 U[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      U[nt] = zero4();
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (lower_has(w, s)) {
+          bf16x8 y[3];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) y[i] = read8<C>(sR[i], 16 * nt + l16, 32 * s + 8 * q4);
+          U[nt] = mfma_parts(tf[s], y, U[nt]);
+        }
+    }
+    load_t(next);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      u32x2 p[3];
+      split4(U[nt] * keep, p);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) write4<C>(sU[i], 16 * nt + l16, 16 * w + 4 * q4, p[i]);
+      if constexpr (SAVE) {
+        float* to = a.us + ((bh * a.seg + ci) * C + 16 * w + 4 * q4) * a.dv + n0 + 16 * nt + l16;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) to[r * a.dv] = U[nt][r];
+      } else {
+        u32x2 o[2];
+        split4(U[nt], o);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) write4<C>(sV[i], 16 * nt + l16, 16 * w + 4 * q4, o[i]);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int st = 0; st < ST; ++st) S[st][nt] *= last;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        bf16x8 y[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) y[i] = read8<C>(sU[i], 16 * nt + l16, 32 * s + 8 * q4);
+#pragma unroll
+        for (int st = 0; st < ST; ++st) {
+          const bf16x8 x[1] = {ktf[st][s]};
+          S[st][nt] = mfma_parts(x, y, S[st][nt]);
+        }
+      }
+      if constexpr (!SAVE) {
+        O[nt] *= eg * a.scale;
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          if (lower_has(w, s)) {
+            bf16x8 y[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) y[i] = read8<C>(sV[i], 16 * nt + l16, 32 * s + 8 * q4);
+            O[nt] = mfma_parts(af[s], y, O[nt]);
+          }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int64_t p = (a.chunk0 + ci) * C + 16 * w + 4 * q4 + r;
+          if (p < L) {
+            bf16_t o;
+            from_f32(O[nt][r], &o);
+            a.out[((b * L + a.sh.token(p)) * a.sh.heads + h) * a.dv + n0 + 16 * nt + l16] = o.bits;
+          }
+        }
+      }
+    }
+    load_a(next), load_kt(next), load_gates(next);
+  }
+  if (a.state_out) {
+#pragma unroll
+    for (int st = 0; st < ST; ++st)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          a.state_out[(bh * DK + 16 * (ST * w + st) + 4 * q4 + r) * a.dv + n0 + 16 * nt + l16] = S[st][nt][r];
+  }
+}
+
+// Up to kStepMax tokens, one after the other, all in fp32: a wavefront per 32 columns of a head's state, which it holds in
+// registers (8 lanes x 4 columns, an eighth of the rows each).
+struct StepArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  const uint16_t* dt;
+  const uint16_t* b;
+  const float* A;
+  const float* dt_bias;
+  const float* state_in;
+  float* state_out;
+  uint16_t* out;
+  Shape sh;
+  int64_t rows, dv;  // rows: batch * heads
+  float scale;
+};
+
+// Sum over the lanes that hold the same columns (lane % 8), in each of them.
+__device__ __forceinline__ float row_parts_sum(float v) {
+  v += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x128, 0xf, 0xf, true));  // row_ror:8
+  auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+
+template <int DK>
+__global__ __launch_bounds__(256) void k_delta_step(StepArgs a) {
+  constexpr int R = DK / 8;  // rows per lane
+  const int lane = threadIdx.x & 63, part = lane >> 3;
+  const int64_t slices = a.dv / 32;
+  const int64_t wave = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (wave >= a.rows * slices) return;
+  const int64_t bh = wave / slices, b = bh / a.sh.heads, h = bh % a.sh.heads, kh = h / (a.sh.heads / a.sh.hk);
+  const int64_t n = wave % slices * 32 + (lane & 7) * 4;
+  const int64_t L = a.sh.L;
+  f32x4 S[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    S[i] = a.state_in ? *reinterpret_cast<const f32x4*>(a.state_in + (bh * DK + part * R + i) * a.dv + n) : zero4();
+  const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
+  bf16x8 kn[R / 8], qn[R / 8];
+  u32x2 vn;
+  uint16_t dtn, bn;
+  auto fetch = [&](int64_t p) {
+    const int64_t t = b * L + a.sh.token(p);
+#pragma unroll
+    for (int i = 0; i < R / 8; ++i) {
+      kn[i] = *reinterpret_cast<const bf16x8*>(a.k + (t * a.sh.hk + kh) * DK + part * R + 8 * i);
+      qn[i] = *reinterpret_cast<const bf16x8*>(a.q + (t * a.sh.hk + kh) * DK + part * R + 8 * i);
+    }
+    vn = *reinterpret_cast<const u32x2*>(a.v + (t * a.sh.heads + h) * a.dv + n);
+    dtn = a.dt[t * a.sh.heads + h];
+    bn = a.b[t * a.sh.heads + h];
+  };
+  fetch(0);
+  for (int64_t p = 0; p < L; ++p) {
+    float k[R], q[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) k[i] = static_cast<float>(kn[i / 8][i % 8]), q[i] = static_cast<float>(qn[i / 8][i % 8]);
+    const f32x4 v = __builtin_convertvector(__builtin_bit_cast(bf16x4, vn), f32x4);
+    const float decay = ex(softplus_f32(bf(dtn) + bias) * A), beta = sigmoid_f32(bf(bn));
+    if (p + 1 < L) fetch(p + 1);
+    f32x4 d = zero4(), o = zero4();
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      S[i] *= decay;
+      d += k[i] * S[i];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] = beta * (v[e] - row_parts_sum(d[e]));
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      S[i] += k[i] * d;
+      o += q[i] * S[i];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = row_parts_sum(o[e]) * a.scale;
+    if (part == 0)
+      *reinterpret_cast<u32x2*>(a.out + ((b * L + a.sh.token(p)) * a.sh.heads + h) * a.dv + n) =
+          __builtin_bit_cast(u32x2, __builtin_convertvector(o, bf16x4));
+  }
+  if (a.state_out) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      *reinterpret_cast<f32x4*>(a.state_out + (bh * DK + part * R + i) * a.dv + n) = S[i];
+  }
+}
+
+template <int DK, bool SAVE>
+void launch_walk(const WalkArgs& a, int tiles, hipStream_t stream) {
+  const int64_t rows = (a.batch * a.sh.heads + 7) / 8 * 8;
+  const dim3 grid(static_cast<unsigned>(rows * (a.dv / (16 * tiles))));
+  if (tiles == 1) hipLaunchKernelGGL((k_delta_walk<DK, 1, SAVE>), grid, dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((k_delta_walk<DK, 2, SAVE>), grid, dim3(256), 0, stream, a);
+}
+
+}  // namespace
+
+hipError_t launch_delta_step(const DeltaArgs& in, hipStream_t stream) {
+  const StepArgs a{static_cast<const uint16_t*>(in.q), static_cast<const uint16_t*>(in.k),
+                   static_cast<const uint16_t*>(in.v), static_cast<const uint16_t*>(in.dt),
+                   static_cast<const uint16_t*>(in.b), in.A, in.dt_bias, in.h_in, in.h_out,
+                   static_cast<uint16_t*>(in.out), Shape{in.seqlen, in.hk, in.heads, in.rev}, in.batch * in.heads,
+                   in.dv, in.scale};
+  const dim3 grid(static_cast<unsigned>((a.rows * (in.dv / 32) + 3) / 4));
+  if (in.dk == 64) hipLaunchKernelGGL((k_delta_step<64>), grid, dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((k_delta_step<128>), grid, dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_delta_prep(const DeltaArgs& in, const Plan& p, int64_t chunk0, int64_t chunks, bool grad, void* ws,
+                             hipStream_t stream) {
+  const Layout lay = make_layout(in.dk, grad);
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  const PrepArgs a{static_cast<const uint16_t*>(in.q), static_cast<const uint16_t*>(in.k),
+                   static_cast<const uint16_t*>(in.dt), static_cast<const uint16_t*>(in.b), in.A, in.dt_bias,
+                   w + p.head_off, w + p.key_off, Shape{in.seqlen, in.hk, in.heads, in.rev}, lay, chunk0, p.seg,
+                   in.scale};
+  const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(in.heads), static_cast<unsigned>(in.batch));
+  if (in.dk == 64) {
+    if (grad) hipLaunchKernelGGL((k_delta_prep<64, true>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((k_delta_prep<64, false>), grid, dim3(256), 0, stream, a);
+  } else {
+    if (grad) hipLaunchKernelGGL((k_delta_prep<128, true>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((k_delta_prep<128, false>), grid, dim3(256), 0, stream, a);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_delta_walk(const DeltaArgs& in, const Plan& p, int64_t chunk0, int64_t chunks, bool save,
+                             const float* state_in, float* state_out, void* ws, hipStream_t stream) {
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  const WalkArgs a{static_cast<const uint16_t*>(in.q), static_cast<const uint16_t*>(in.k),
+                   static_cast<const uint16_t*>(in.v), static_cast<uint16_t*>(in.out), w + p.head_off, w + p.key_off,
+                   state_in, state_out, reinterpret_cast<float*>(w + p.s_off), reinterpret_cast<float*>(w + p.u_off),
+                   Shape{in.seqlen, in.hk, in.heads, in.rev}, make_layout(in.dk, save), in.batch, in.dv, chunk0, chunks,
+                   p.seg, in.scale};
+  if (in.dk == 64) {
+    if (save) launch_walk<64, true>(a, p.tiles, stream);
+    else launch_walk<64, false>(a, p.tiles, stream);
+  } else {
+    if (save) launch_walk<128, true>(a, p.tiles, stream);
+    else launch_walk<128, false>(a, p.tiles, stream);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_delta_fwd(const DeltaArgs& in, const Plan& p, void* ws, hipStream_t stream) {
+  float* carry = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + p.carry_off);
+  const float* from = in.h_in;
+  for (int64_t c0 = 0; c0 < p.nchunk; c0 += p.seg) {
+    const int64_t n = p.nchunk - c0 < p.seg ? p.nchunk - c0 : p.seg;
+    float* to = c0 + n == p.nchunk ? in.h_out : carry;
+    hipError_t e = launch_delta_prep(in, p, c0, n, false, ws, stream);
+    if (e != hipSuccess) return e;
+    e = launch_delta_walk(in, p, c0, n, false, from, to, ws, stream);
+    if (e != hipSuccess) return e;
+    from = carry;
+  }
+  return hipSuccess;
+}
+
+}  // namespace delta
+}  // namespace bimamba

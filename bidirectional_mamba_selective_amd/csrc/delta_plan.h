@@ -1,0 +1,101 @@
+// Host-side decomposition of the gated delta rule: chunks of tokens, the operands that the walk over them reads, and the
+// layout of the workspace.  Pure host code: no HIP calls.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "plan.h"
+
+namespace bimamba {
+namespace delta {
+
+constexpr int64_t kC = 64;            // tokens per chunk
+constexpr int64_t kStepMax = 16;      // tokens up to which the forward pass goes token by token
+constexpr size_t kFragBytes = 1024;   // one matrix operand of 16 x 32 bf16 values, 16 bytes a lane
+constexpr int64_t kTriFrags = 6;      // operands that a triangular 64 x 64 matrix has (of 8; the others are zero)
+constexpr int64_t kGateFloats = 320;  // per (head, chunk): five rows of 64, see k_delta_prep
+
+// What the preparing kernel leaves for one (batch element, head, chunk), in bytes from the start of its record.
+struct Layout {
+  size_t gates, t, tt, a, at, bytes;  // forward: t, a; backward: t, tt, at
+  size_t key_bytes;                   // per (batch element, key head, chunk): K^T, backward also Q^T
+};
+
+inline Layout make_layout(int64_t dk, bool grad) {
+  Layout l{};
+  size_t off = kGateFloats * 4;
+  l.t = off, off += kTriFrags * 3 * kFragBytes;
+  if (grad) {
+    l.tt = off, off += kTriFrags * 3 * kFragBytes;
+    l.at = off, off += kTriFrags * 3 * kFragBytes;
+  } else {
+    l.a = off, off += kTriFrags * 2 * kFragBytes;
+  }
+  l.bytes = align256(off);
+  l.key_bytes = static_cast<size_t>(dk / 16) * 2 * kFragBytes * (grad ? 2 : 1);
+  return l;
+}
+
+// Columns of a value head that one workgroup of a walk takes, in tiles of 16: few, so that the state of a head is spread
+// over many compute units; more once there are heads enough.
+inline int walk_tiles(int64_t heads, int64_t dv) {
+  const int64_t tiles = dv / 16;
+  return heads * tiles <= 512 ? 1 : 2;
+}
+
+struct Plan {
+  int64_t nchunk;  // ceil(seqlen / kC)
+  int64_t seg;     // chunks prepared at a time (forward); nchunk (backward)
+  int tiles;
+  size_t head_off, key_off, carry_off, s_off, ds_off, u_off, dr_off, part_off, total;
+};
+
+// Forward: the operands of `seg` chunks of every head at a time, so that they are read from the last-level cache (256 MiB)
+// rather than from memory; the states between two segments.
+constexpr size_t kSegBytes = size_t{96} << 20;
+
+inline Plan make_fwd_plan(int64_t batch, int64_t seqlen, int64_t hk, int64_t heads, int64_t dk, int64_t dv) {
+  Plan p{};
+  p.nchunk = (seqlen + kC - 1) / kC;
+  p.tiles = walk_tiles(batch * heads, dv);
+  if (seqlen <= kStepMax) return p;
+  const Layout l = make_layout(dk, false);
+  const size_t per_chunk = static_cast<size_t>(batch) * (heads * l.bytes + hk * l.key_bytes);
+  int64_t seg = static_cast<int64_t>(kSegBytes / per_chunk);
+  seg = seg < 8 ? 8 : seg;
+  // segments of equal length
+  const int64_t n = (p.nchunk + seg - 1) / seg;
+  p.seg = (p.nchunk + n - 1) / n;
+  p.head_off = 0;
+  size_t off = static_cast<size_t>(batch) * heads * p.seg * l.bytes;
+  p.key_off = off, off += align256(static_cast<size_t>(batch) * hk * p.seg * l.key_bytes);
+  p.carry_off = off;
+  if (p.seg < p.nchunk) off += align256(static_cast<size_t>(batch) * heads * dk * dv * 4);
+  p.total = off;
+  return p;
+}
+
+// Backward: the operands, both states (entering from the left, gradient entering from the right), U and the gradient of
+// its right-hand side for every chunk, and the chunks' partial sums of the gradients of A and dt_bias.
+inline Plan make_bwd_plan(int64_t batch, int64_t seqlen, int64_t hk, int64_t heads, int64_t dk, int64_t dv) {
+  Plan p{};
+  p.nchunk = (seqlen + kC - 1) / kC;
+  p.seg = p.nchunk;
+  p.tiles = walk_tiles(batch * heads, dv);
+  const Layout l = make_layout(dk, true);
+  const size_t hc = static_cast<size_t>(batch) * heads * p.nchunk;
+  p.head_off = 0;
+  size_t off = hc * l.bytes;
+  p.key_off = off, off += align256(static_cast<size_t>(batch) * hk * p.nchunk * l.key_bytes);
+  p.s_off = off, off += hc * dk * dv * 4;
+  p.ds_off = off, off += hc * dk * dv * 4;
+  p.u_off = off, off += hc * kC * dv * 4;
+  p.dr_off = off, off += hc * kC * dv * 4;
+  p.part_off = off, off += align256(hc * 8);
+  p.total = off;
+  return p;
+}
+
+}  // namespace delta
+}  // namespace bimamba

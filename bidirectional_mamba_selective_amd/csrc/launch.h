@@ -6,6 +6,7 @@
 
 #include "bwd_plan.h"
 #include "conv_bwd_plan.h"
+#include "delta_plan.h"
 #include "plan.h"
 #include "ssd_plan.h"
 
@@ -86,6 +87,7 @@ struct AdalnArgs {
   float eps;
   int rms;
   int io_dtype;
+  float* scales = nullptr;  // forward only: given, out is e4m3 with these scales
 };
 
 struct AdalnGrads {
@@ -103,6 +105,70 @@ hipError_t launch_adaln_fwd(const AdalnArgs& a, hipStream_t stream);
 hipError_t launch_adaln_bwd(const AdalnArgs& a, const AdalnGrads& g, void* workspace, hipStream_t stream);
 
 }  // namespace adaln
+
+namespace delta {
+
+// The gated delta rule, one direction; null pointers as in the C ABI.
+struct DeltaArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* dt;
+  const float* A;
+  const void* b;
+  const float* dt_bias;
+  const float* h_in;
+  float* h_out;
+  void* out;
+  int64_t batch, seqlen, hk, heads, dk, dv;
+  float scale;
+  int rev;
+};
+
+struct DeltaGrads {
+  const void* dout;
+  const float* dh_out;  // null: 0
+  void* dq;
+  void* dk;
+  void* dv;
+  void* ddt;
+  float* dA;
+  void* db;
+  float* ddt_bias;  // null: not written
+  float* dh_in;     // null: not written
+};
+
+// Forward: token by token up to kStepMax tokens (no workspace), by chunks above.
+hipError_t launch_delta_step(const DeltaArgs& a, hipStream_t stream);
+hipError_t launch_delta_fwd(const DeltaArgs& a, const Plan& p, void* workspace, hipStream_t stream);
+hipError_t launch_delta_bwd(const DeltaArgs& a, const DeltaGrads& g, const Plan& p, void* workspace,
+                            hipStream_t stream);
+
+// Its parts over chunks [chunk0, chunk0 + chunks): the chunks' operands, and the walk over them; `save` keeps for the
+// backward pass what it meets and computes no output.
+hipError_t launch_delta_prep(const DeltaArgs& a, const Plan& p, int64_t chunk0, int64_t chunks, bool grad,
+                             void* workspace, hipStream_t stream);
+hipError_t launch_delta_walk(const DeltaArgs& a, const Plan& p, int64_t chunk0, int64_t chunks, bool save,
+                             const float* state_in, float* state_out, void* workspace, hipStream_t stream);
+
+}  // namespace delta
+
+namespace proj {
+
+// Product of e4m3 rows x [m, k] and weights w [n, k] with block scales; out [m, n].
+struct ProjArgs {
+  const void* x;
+  const float* xs;
+  const void* w;
+  const float* ws;
+  void* out;
+  int64_t m, n, k;
+  int out_dtype;
+};
+
+hipError_t launch_proj(const ProjArgs& a, hipStream_t stream);
+
+}  // namespace proj
 
 namespace conv {
 

@@ -408,6 +408,20 @@ int bimamba_adaln_fwd(const void* x, const void* branch, const float* post_weigh
                       const float* gamma, const float* beta, void* h, void* out, int64_t batch, int64_t seqlen,
                       int64_t d_model, int64_t mod_rows, float eps, int io_dtype, uint32_t flags, hipStream_t stream);
 
+/* bimamba_adaln_fwd with out in 8 bits, as the projection that follows it reads it (bimamba_proj_fp8): with
+ * y the value that bimamba_adaln_fwd rounds to out, and for each row and each run of 128 columns
+ *   scale = max(max |y|, 2^-100) / 448,   out = y / scale rounded to nearest even e4m3
+ * (OCP e4m3: 448 is its largest value; y / scale is formed as y * (1 / scale)).  With beta NULL and RMS_NORM this is the
+ * root-mean-square norm behind the residual's addition.
+ *   out: [batch, seqlen, d_model], one byte a value; scales: [batch, seqlen, d_model / 128] fp32.
+ * A NaN makes out NaN where bimamba_adaln_fwd's would be one; the scales pass over it.
+ * d_model must be a multiple of 128; everything else is as for bimamba_adaln_fwd, whose backward pass is also this one's
+ * where the rounding to 8 bits is passed over. */
+int bimamba_adaln_fwd_fp8(const void* x, const void* branch, const float* post_weight, const float* gate,
+                          const float* gamma, const float* beta, void* h, void* out, float* scales, int64_t batch,
+                          int64_t seqlen, int64_t d_model, int64_t mod_rows, float eps, int io_dtype, uint32_t flags,
+                          hipStream_t stream);
+
 /* Bytes of device workspace bimamba_adaln_bwd needs for this shape; 0 for an
  * unsupported shape. */
 size_t bimamba_adaln_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t d_model);
@@ -433,6 +447,66 @@ int bimamba_adaln_bwd(const void* dout, const void* dres, const void* h, const v
                       float* dgate, float* dgamma, float* dbeta, int64_t batch, int64_t seqlen, int64_t d_model,
                       int64_t mod_rows, float eps, int io_dtype, uint32_t flags, void* workspace,
                       size_t workspace_bytes, hipStream_t stream);
+
+/* ---- Projection in 8 bits --------------------------------------------------
+ * The dense product of a block's projections on 8-bit operands (OCP e4m3) with a scale for each block of 128 inputs:
+ *   out[m,n] = sum_j x_scales[m,j] w_scales[n/128,j] sum_{k = 128 j}^{128 j + 127} x[m,k] w[n,k]
+ * x and x_scales are what bimamba_adaln_fwd_fp8 writes (any row count: a batch of sequences, a block, one token); w is
+ * quantised once, one scale for each 128 x 128 weights (n / 128 rounded down; the last row of scales serves the rest of
+ * the outputs).  Products are exact, sums fp32, out is rounded to nearest even once.
+ *   x: [rows, d_in], w: [d_out, d_in], one byte a value; x_scales: [rows, d_in / 128] fp32;
+ *   w_scales: [(d_out + 127) / 128, d_in / 128] fp32; out: [rows, d_out], out_dtype BIMAMBA_BF16 or BIMAMBA_F32.
+ * Supported: d_in a multiple of 128, d_out of 8, both at most 2^22, 1 <= rows <= 2^31.  x, w and out 16-byte aligned,
+ * scales 4.  out must not overlap an input.  No workspace. */
+int bimamba_proj_fp8(const void* x, const float* x_scales, const void* w, const float* w_scales, void* out,
+                     int64_t rows, int64_t d_out, int64_t d_in, int out_dtype, hipStream_t stream);
+
+/* ---- Gated delta rule ------------------------------------------------------
+ * A mixer whose state is a headdim_k x headdim_v matrix per head, decayed by each token and corrected towards its value
+ * along its key; one direction of a layer with untied directions per call (flags FWD_ONLY: tokens 0 .. L-1, REV_ONLY:
+ * L-1 .. 0; exactly one of them).  Per head h, with key head h / (nheads / nheads_k), in the direction's order:
+ *   delta = softplus(dt[t,h] + dt_bias[h]),  a = exp(delta * A[h]),  beta = sigmoid(b[t,h])
+ *   H     = a H_before,   H_t = H + beta k_t (v_t - H^T k_t)^T,   out[t,h,:] = scale * H_t^T q_t
+ *   (the state before the first token is h_in, or zeros)
+ * Layouts: q, k [batch, seqlen, nheads_k, headdim_k]; v, out [batch, seqlen, nheads, headdim_v]; dt, b [batch, seqlen,
+ * nheads]; A, dt_bias [nheads] fp32; h_in, h_out [batch, nheads, headdim_k, headdim_v] fp32, the state before the
+ * direction's first and after its last token (the cache of block decoding: a block, or a single token, is a call with both; h_out may
+ * equal h_in).  dt_bias, h_in and h_out may be NULL (zeros; not written).
+ * The layer is meant for A <= 0 and keys of about unit length; the states grow without bound otherwise.  Decays below e^-256 per token
+ * count as e^-256 (zero in fp32).  b = -inf and dt = -inf are allowed and make a token that leaves the state as it is
+ * (a padded place: with finite q, k, v there); other non-finite values make the results of their batch element and head
+ * non-finite from the 64-token chunk on in which they stand.
+ * Supported: io_dtype BIMAMBA_BF16 (q, k, v, dt, b, out), headdim_k and headdim_v 64 or 128, nheads a multiple of
+ * nheads_k, batch and nheads at most 65535, batch * nheads at most 10^6.  q, k, v, out, h_in, h_out 16-byte aligned, dt
+ * and b 2, A and dt_bias 4.  States and all sums are carried at fp32 accuracy.
+ * Up to 16 tokens need no workspace (bimamba_delta_fwd_workspace_bytes returns 0, workspace may be NULL); otherwise it is
+ * 256-byte aligned and its contents on entry are ignored.  No output may overlap an input (h_out equal to h_in excepted),
+ * another output or the workspace. */
+size_t bimamba_delta_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads_k, int64_t nheads,
+                                         int64_t headdim_k, int64_t headdim_v);
+
+int bimamba_delta_fwd(const void* q, const void* k, const void* v, const void* dt, const float* A, const void* b,
+                      const float* dt_bias, const float* h_in, float* h_out, void* out, int64_t batch, int64_t seqlen,
+                      int64_t nheads_k, int64_t nheads, int64_t headdim_k, int64_t headdim_v, float scale, int io_dtype,
+                      uint32_t flags, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Backward pass of bimamba_delta_fwd: the gradients of its inputs for dout, the gradient of out, and dh_out, that of
+ * h_out (NULL = 0).  Nothing of the forward call is needed: everything is recomputed from its inputs.
+ *   dq, dk, dv, ddt, db: like their inputs (bf16, rounded once; dq and dk summed over the heads that share them);
+ *   dA, ddt_bias [nheads] fp32, summed over batch and tokens; dh_in: the gradient of h_in.
+ * ddt_bias and dh_in may be NULL (not written); they may be asked for also where dt_bias or h_in is NULL.  dh_in may
+ * equal dh_out.  All sums run in a fixed order: two calls on the same inputs give the same bits.  Shapes, types, flags and
+ * alignment are as for bimamba_delta_fwd; workspace 256-byte aligned, contents ignored on entry.  No output may overlap
+ * an input (dh_in equal to dh_out excepted), another output or the workspace. */
+size_t bimamba_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads_k, int64_t nheads,
+                                         int64_t headdim_k, int64_t headdim_v);
+
+int bimamba_delta_bwd(const void* dout, const void* q, const void* k, const void* v, const void* dt, const float* A,
+                      const void* b, const float* dt_bias, const float* h_in, const float* dh_out, void* dq, void* dk,
+                      void* dv, void* ddt, float* dA, void* db, float* ddt_bias, float* dh_in, int64_t batch,
+                      int64_t seqlen, int64_t nheads_k, int64_t nheads, int64_t headdim_k, int64_t headdim_v,
+                      float scale, int io_dtype, uint32_t flags, void* workspace, size_t workspace_bytes,
+                      hipStream_t stream);
 
 #ifdef __cplusplus
 }
