@@ -24,8 +24,6 @@ namespace bimamba {
 namespace delta {
 namespace {
 
-constexpr int C = static_cast<int>(kC);
-
 struct RWalkArgs {
   const uint16_t* dout;
   const uint16_t* k;
@@ -50,181 +48,233 @@ __device__ __forceinline__ bool place(int64_t slices, int64_t rows, int64_t* row
   return *row < rows;
 }
 
+// One workgroup: 16 NT columns of the state's gradient.  Four wavefronts carry it as those of the forward walk carry the
+// state (K dS, T^T dU, K^T dR).  What does not depend on it (A^T dO and Q^T dO) is made by four more, a chunk ahead,
+// between the same barriers, and waits in LDS.
 template <int DK, int NT>
-__global__ __launch_bounds__(256) void k_delta_rwalk(RWalkArgs a) {
-  constexpr int KS = DK / 32, ST = DK / 64, NS = 16 * NT;
-  __shared__ __align__(16) uint16_t sS[3][NS * DK], sD[NS * C], sE[3][NS * C], sR[3][NS * C], sU[3][NS * C];
-  const int lane = threadIdx.x & 63, l16 = lane & 15, q4 = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+__global__ __launch_bounds__(512, 2) void k_delta_rwalk(RWalkArgs a) {
+  constexpr int ST = DK / 64, NS = 16 * NT, kB = static_cast<int>(kFragBytes);
+  typedef typename Own<ST>::type own_t;
+  __shared__ __align__(16) float sP[NT][4][4][256], sX[2][NT][4][ST + 1][256];
+  __shared__ __align__(16) uint16_t sD[NS * C], sE[3][NS * C], sR[3][NS * C], sU[3][NS * C];
+  const int lane = threadIdx.x & 63, l16 = lane & 15, q4 = lane >> 4, lane16 = lane * 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave & 3;
   int64_t bh, slice;
   if (!place(a.dv / NS, a.batch * a.sh.heads, &bh, &slice)) return;
   const int64_t b = bh / a.sh.heads, h = bh % a.sh.heads, kh = h / (a.sh.heads / a.sh.hk);
-  const int64_t L = a.sh.L, n0 = slice * NS;
+  const int n0 = static_cast<int>(slice) * NS, dv = static_cast<int>(a.dv), chunks = static_cast<int>(a.chunks);
   const unsigned char* rec = a.heads + bh * a.chunks * a.lay.bytes;
   const unsigned char* key = a.keys + (b * a.sh.hk + kh) * a.chunks * a.lay.key_bytes;
+  const int rec_bytes = static_cast<int>(a.lay.bytes), key_bytes = static_cast<int>(a.lay.key_bytes);
+  const int key_pitch = static_cast<int>(a.sh.hk) * DK * 2, val_pitch = static_cast<int>(a.sh.heads) * dv * 2;
+  int val_row[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) val_row[r] = row_offset(a.sh, val_pitch, 16 * w + 4 * q4 + r) + 2 * l16;
+  auto gates4 = [&](__amdgpu_buffer_rsrc_t r, int row) {
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, 16 * q4, 4 * C * row + 64 * w, 0));
+  };
+  auto head_record = [&](int ci) { return record(rec + static_cast<int64_t>(ci) * rec_bytes, a.lay.bytes); };
+  auto load_tri = [&](int ci, size_t off, bf16x8(&f)[2][3]) {
+    const __amdgpu_buffer_rsrc_t r = head_record(ci);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      if (upper_has(w, s))
+#pragma unroll
+        for (int i = 0; i < 3; ++i) f[s][i] = record_frag(r, static_cast<int>(off) + upper_at(w, s) * 3 * kB, i, lane16);
+  };
+  // tile rows of K^T (which 0) or Q^T (1)
+  auto load_keys = [&](int ci, int which, bf16x8(&f)[ST][2]) {
+    const __amdgpu_buffer_rsrc_t r = record(key + static_cast<int64_t>(ci) * key_bytes, a.lay.key_bytes);
+#pragma unroll
+    for (int st = 0; st < ST; ++st)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) f[st][s] = record_frag(r, (which * (DK / 8) + ST * w * 2) * kB, 2 * st + s, lane16);
+  };
 
+  if (wave >= 4) {
+    const uint16_t* o0 = a.dout + (b * a.sh.L * a.sh.heads + h) * dv + n0;
+    bf16x8 af[2][3], qtf[ST][2];
+    uint16_t vv[NT][4];
+    f32x4 eg;
+    auto load = [&](int ci) {
+      const Rows o = chunk_rows(o0, a.sh, val_pitch, 2 * NS, ci * C);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) vv[nt][r] = row_load1(o, val_row[r] + 32 * nt);
+      eg = gates4(head_record(ci), 0);
+      load_tri(ci, a.lay.at, af);
+      load_keys(ci, 1, qtf);
+    };
+    auto put = [&]() {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const u32x2 raw = {vv[nt][0] | static_cast<uint32_t>(vv[nt][1]) << 16,
+                           vv[nt][2] | static_cast<uint32_t>(vv[nt][3]) << 16};
+        write4<C>(sD, 16 * nt + l16, 16 * w + 4 * q4, raw);
+        u32x2 p[3];
+        split4(f32x4{bf(vv[nt][0]), bf(vv[nt][1]), bf(vv[nt][2]), bf(vv[nt][3])} * (eg * a.scale), p);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) write4<C>(sE[i], 16 * nt + l16, 16 * w + 4 * q4, p[i]);
+      }
+    };
+    auto products = [&](int ci) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        f32x4 x[3] = {zero4(), zero4(), zero4()}, y[ST][3];
+#pragma unroll
+        for (int st = 0; st < ST; ++st) y[st][0] = y[st][1] = y[st][2] = zero4();
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const bf16x8 d = read8<C>(sD, 16 * nt + l16, 32 * s + 8 * q4);
+          bf16x8 e[3];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) e[i] = read8<C>(sE[i], 16 * nt + l16, 32 * s + 8 * q4);
+          if (upper_has(w, s))
+#pragma unroll
+            for (int i = 0; i < 3; ++i) x[i] = mfma(af[s][i], d, x[i]);
+#pragma unroll
+          for (int st = 0; st < ST; ++st) mfma_three(qtf[st][s], e, y[st]);
+        }
+        *reinterpret_cast<f32x4*>(&sX[ci & 1][nt][w][ST][4 * lane]) = sum3(x);
+#pragma unroll
+        for (int st = 0; st < ST; ++st) *reinterpret_cast<f32x4*>(&sX[ci & 1][nt][w][st][4 * lane]) = sum3(y[st]);
+      }
+    };
+    load(chunks - 1);
+    put();
+    lds_barrier();
+    products(chunks - 1);
+    if (chunks > 1) load(chunks - 2);
+    lds_barrier();
+    for (int ci = chunks - 1; ci >= 0; --ci) {
+      if (ci > 0) put();
+      lds_barrier();
+      if (ci > 0) products(ci - 1);
+      if (ci > 1) load(ci - 2);
+      lds_barrier();
+      lds_barrier();
+    }
+    return;
+  }
+
+  const uint16_t* k0 = a.k + (b * a.sh.L * a.sh.hk + kh) * DK + 16 * ST * w;
+  uint16_t* dv0 = a.dv_out + (b * a.sh.L * a.sh.heads + h) * dv + n0;
+  const int64_t state0 = (bh * DK + state_row<ST>(w, 0, 4 * q4)) * dv + n0 + l16;
   f32x4 S[ST][NT];
 #pragma unroll
   for (int st = 0; st < ST; ++st)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t i = (bh * DK + 16 * (ST * w + st) + 4 * q4 + r) * a.dv + n0 + 16 * nt + l16;
-        S[st][nt][r] = a.dh_out ? a.dh_out[i] : 0.0f;
-      }
+      for (int r = 0; r < 4; ++r) S[st][nt][r] = a.dh_out ? a.dh_out[state0 + (4 * st + r) * dv + 16 * nt] : 0.0f;
 
-  bf16x8 kf[KS], tf[2][3], af[2][3], ktf[ST][2], qtf[ST][2];
-  uint16_t vv[NT][4];
+  own_t kf[4];
+  bf16x8 tf[2][3], ktf[ST][2];
   f32x4 eg, keep;
   float last;
-  auto load_k = [&](int64_t ci) {
-    const int64_t p = ci * C + 16 * w + l16;
-    const uint16_t* row = a.k + ((b * L + a.sh.token(p < L ? p : L - 1)) * a.sh.hk + kh) * DK + 8 * q4;
+  int key_row[4];
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      kf[s] = *reinterpret_cast<const bf16x8*>(row + 32 * s);
-      if (p >= L) kf[s] = zero8();
-    }
+  for (int i = 0; i < 4; ++i) key_row[i] = row_offset(a.sh, key_pitch, 16 * i + l16) + 8 * ST * q4;
+  auto load_k = [&](int ci) {
+    const Rows k = chunk_rows(k0, a.sh, key_pitch, 32 * ST, ci * C);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) row_load(k, key_row[i], &kf[i]);
   };
-  auto load_do = [&](int64_t ci) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t p = ci * C + 16 * w + 4 * q4 + r;
-      const uint16_t* row = a.dout + ((b * L + a.sh.token(p < L ? p : L - 1)) * a.sh.heads + h) * a.dv + n0 + l16;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) vv[nt][r] = p < L ? row[16 * nt] : static_cast<uint16_t>(0);
-    }
+  auto load_gates = [&](int ci) {
+    const __amdgpu_buffer_rsrc_t r = head_record(ci);
+    eg = gates4(r, 0);
+    keep = gates4(r, 1);
+    last = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, 4 * (C - 1), 0, 0));
   };
-  auto load_tri = [&](int64_t ci, size_t off, bf16x8(&f)[2][3]) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-      if (upper_has(w, s))
-#pragma unroll
-        for (int i = 0; i < 3; ++i) f[s][i] = load_frag(rec + ci * a.lay.bytes + off, upper_at(w, s) * 3 + i, lane);
-  };
-  auto load_keys = [&](int64_t ci) {
-#pragma unroll
-    for (int st = 0; st < ST; ++st)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        ktf[st][s] = load_frag(key + ci * a.lay.key_bytes, (ST * w + st) * 2 + s, lane);
-        qtf[st][s] = load_frag(key + ci * a.lay.key_bytes, DK / 8 + (ST * w + st) * 2 + s, lane);
-      }
-  };
-  auto load_gates = [&](int64_t ci) {
-    const float* g = reinterpret_cast<const float*>(rec + ci * a.lay.bytes);
-    eg = *reinterpret_cast<const f32x4*>(g + 16 * w + 4 * q4);
-    keep = *reinterpret_cast<const f32x4*>(g + C + 16 * w + 4 * q4);
-    last = g[C - 1];
-  };
-  {
-    const int64_t c = a.chunks - 1;
-    load_k(c), load_do(c), load_tri(c, a.lay.tt, tf), load_tri(c, a.lay.at, af), load_keys(c), load_gates(c);
-  }
+  load_k(chunks - 1), load_tri(chunks - 1, a.lay.tt, tf), load_gates(chunks - 1), load_keys(chunks - 1, 0, ktf);
+  lds_barrier();
+  lds_barrier();
 
-  for (int64_t ci = a.chunks - 1; ci >= 0; --ci) {
-    const int64_t next = ci > 0 ? ci - 1 : 0;
+  for (int ci = chunks - 1; ci >= 0; --ci) {
+    const int next = ci > 0 ? ci - 1 : 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      own_t own[3];
+      split_own<ST, NT>(S, nt, own);
+      f32x4 P[4];
 #pragma unroll
-      for (int st = 0; st < ST; ++st) {
-        u32x2 p[3];
-        split4(S[st][nt], p);
+      for (int i = 0; i < 4; ++i) P[i] = zero4();
 #pragma unroll
-        for (int i = 0; i < 3; ++i) write4<DK>(sS[i], 16 * nt + l16, 16 * (ST * w + st) + 4 * q4, p[i]);
-        float* to = a.dstates + ((bh * a.chunks + ci) * DK + 16 * (ST * w + st) + 4 * q4) * a.dv + n0 + 16 * nt + l16;
+      for (int j = 2; j >= 0; --j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) to[r * a.dv] = S[st][nt][r];
-      }
-      const u32x2 raw = {vv[nt][0] | static_cast<uint32_t>(vv[nt][1]) << 16,
-                         vv[nt][2] | static_cast<uint32_t>(vv[nt][3]) << 16};
-      write4<C>(sD, 16 * nt + l16, 16 * w + 4 * q4, raw);
-      u32x2 p[3];
-      split4(__builtin_convertvector(__builtin_bit_cast(bf16x4, raw), f32x4) * (eg * a.scale), p);
+        for (int i = 0; i < 4; ++i) P[i] = mfma_own(kf[i], own[j], P[i]);
 #pragma unroll
-      for (int i = 0; i < 3; ++i) write4<C>(sE[i], 16 * nt + l16, 16 * w + 4 * q4, p[i]);
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4*>(&sP[nt][w][i][4 * lane]) = P[i];
+      float* to = a.dstates + ((bh * a.chunks + ci) * DK + state_row<ST>(w, 0, 4 * q4)) * dv + n0 + 16 * nt + l16;
+#pragma unroll
+      for (int st = 0; st < ST; ++st)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) to[(4 * st + r) * dv] = S[st][nt][r];
     }
-    load_do(next);
-    __syncthreads();
-    f32x4 U[NT];
+    load_k(next);
+    lds_barrier();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      U[nt] = zero4();
+      f32x4 p[4];
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const bf16x8 x[1] = {kf[s]};
-        bf16x8 y[3];
+      for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const f32x4*>(&sP[nt][i][w][4 * lane]);
+      const f32x4 x = *reinterpret_cast<const f32x4*>(&sX[ci & 1][nt][w][ST][4 * lane]);
+      u32x2 y[3];
+      split4(((p[0] + p[1]) + (p[2] + p[3])) * keep + x, y);
 #pragma unroll
-        for (int i = 0; i < 3; ++i) y[i] = read8<DK>(sS[i], 16 * nt + l16, 32 * s + 8 * q4);
-        U[nt] = mfma_parts(x, y, U[nt]);
-      }
-      U[nt] *= keep;
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (upper_has(w, s)) {
-          const bf16x8 y[1] = {read8<C>(sD, 16 * nt + l16, 32 * s + 8 * q4)};
-          U[nt] = mfma_parts(af[s], y, U[nt]);
-        }
-      u32x2 p[3];
-      split4(U[nt], p);
-#pragma unroll
-      for (int i = 0; i < 3; ++i) write4<C>(sR[i], 16 * nt + l16, 16 * w + 4 * q4, p[i]);
+      for (int i = 0; i < 3; ++i) write4<C>(sR[i], 16 * nt + l16, 16 * w + 4 * q4, y[i]);
     }
-    load_k(next), load_tri(next, a.lay.at, af);
-    __syncthreads();
+    lds_barrier();
+    f32x4 R[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      f32x4 R = zero4();
+      f32x4 u[3] = {zero4(), zero4(), zero4()};
 #pragma unroll
       for (int s = 0; s < 2; ++s)
         if (upper_has(w, s)) {
           bf16x8 y[3];
 #pragma unroll
           for (int i = 0; i < 3; ++i) y[i] = read8<C>(sR[i], 16 * nt + l16, 32 * s + 8 * q4);
-          R = mfma_parts(tf[s], y, R);
+          mfma_three(tf[s], y, u);
         }
+      R[nt] = sum3(u);
       u32x2 p[3];
-      split4(-eg * R, p);
+      split4(-eg * R[nt], p);
 #pragma unroll
       for (int i = 0; i < 3; ++i) write4<C>(sU[i], 16 * nt + l16, 16 * w + 4 * q4, p[i]);
-      float* to = a.drs + ((bh * a.chunks + ci) * C + 16 * w + 4 * q4) * a.dv + n0 + 16 * nt + l16;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        to[r * a.dv] = R[r];
-        const int64_t t = ci * C + 16 * w + 4 * q4 + r;
-        if (t < L) {
-          bf16_t o;
-          from_f32(R[r], &o);
-          a.dv_out[((b * L + a.sh.token(t)) * a.sh.heads + h) * a.dv + n0 + 16 * nt + l16] = o.bits;
-        }
-      }
     }
     load_tri(next, a.lay.tt, tf);
-    __syncthreads();
+    const float decay = last;
+    load_gates(next);
+    lds_barrier();
+    const Rows out = chunk_rows(dv0, a.sh, val_pitch, 2 * NS, ci * C);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      f32x4 add[ST][3];
 #pragma unroll
-      for (int st = 0; st < ST; ++st) S[st][nt] *= last;
+      for (int st = 0; st < ST; ++st) {
+        add[st][0] = *reinterpret_cast<const f32x4*>(&sX[ci & 1][nt][w][st][4 * lane]);
+        add[st][1] = add[st][2] = zero4();
+      }
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        bf16x8 y[3], z[3];
+        bf16x8 y[3];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          y[i] = read8<C>(sU[i], 16 * nt + l16, 32 * s + 8 * q4);
-          z[i] = read8<C>(sE[i], 16 * nt + l16, 32 * s + 8 * q4);
-        }
+        for (int i = 0; i < 3; ++i) y[i] = read8<C>(sU[i], 16 * nt + l16, 32 * s + 8 * q4);
 #pragma unroll
-        for (int st = 0; st < ST; ++st) {
-          const bf16x8 x[1] = {ktf[st][s]}, u[1] = {qtf[st][s]};
-          S[st][nt] = mfma_parts(x, y, S[st][nt]);
-          S[st][nt] = mfma_parts(u, z, S[st][nt]);
-        }
+        for (int st = 0; st < ST; ++st) mfma_three(ktf[st][s], y, add[st]);
+      }
+#pragma unroll
+      for (int st = 0; st < ST; ++st) S[st][nt] = S[st][nt] * decay + sum3(add[st]);
+      float* to = a.drs + ((bh * a.chunks + ci) * C + 16 * w + 4 * q4) * dv + n0 + 16 * nt + l16;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        to[r * dv] = R[nt][r];
+        row_store1(out, val_row[r] + 32 * nt, R[nt][r]);
       }
     }
-    load_keys(next), load_gates(next);
-    // sE and sD are written again before the next barrier
-    __syncthreads();
+    load_keys(next, 0, ktf);
   }
   if (a.dh_in) {
 #pragma unroll
@@ -232,8 +282,7 @@ __global__ __launch_bounds__(256) void k_delta_rwalk(RWalkArgs a) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          a.dh_in[(bh * DK + 16 * (ST * w + st) + 4 * q4 + r) * a.dv + n0 + 16 * nt + l16] = S[st][nt][r];
+        for (int r = 0; r < 4; ++r) a.dh_in[state0 + (4 * st + r) * dv + 16 * nt] = S[st][nt][r];
   }
 }
 
@@ -290,7 +339,7 @@ __device__ __forceinline__ float sum_rows(float v) {
 
 template <int DK, int DV>
 __global__ __launch_bounds__(256) void k_delta_grads(GradArgs a) {
-  constexpr int KS = DK / 32, VS = DV / 32, KT = DK / 16, kRow = DK + 8, kPitch = C + 1;
+  constexpr int KS = DK / 32, ST = DK / 64, VS = DV / 32, KT = DK / 16, kRow = DK + 8, kPitch = C + 1;
   __shared__ __align__(16) uint16_t sD1[2][C * C], sD1t[2][C * C], sD2[2][C * C], sD2t[2][C * C];
   __shared__ __align__(16) uint16_t sQ[C * kRow], sK[C * kRow];
   __shared__ float sP[C * kPitch];
@@ -321,7 +370,7 @@ __global__ __launch_bounds__(256) void k_delta_grads(GradArgs a) {
   for (int64_t g = 0; g < share; ++g) {
     const int64_t h = kh * share + g, bh = b * a.sh.heads + h, hc = bh * a.chunks + ci;
     const float* gates = reinterpret_cast<const float*>(a.heads + hc * a.lay.bytes);
-    __syncthreads();  // the previous head's readers of what is written here
+    lds_barrier();  // the previous head's readers of what is written here
     if (w == 0) sEg[lane] = gates[lane], sKeep[lane] = gates[C + lane];
     if (w == 1) sHi[lane] = gates[2 * C + lane], sLo[lane] = gates[3 * C + lane];
     // this wavefront's rows of dO, dR and U as operands
@@ -346,7 +395,7 @@ __global__ __launch_bounds__(256) void k_delta_grads(GradArgs a) {
       dot = sum_rows(dot);
       if (q4 == 0) sDb[16 * w + l16] = dot;
     }
-    __syncthreads();
+    lds_barrier();
     const f32x4 eg = *reinterpret_cast<const f32x4*>(sEg + 16 * w + 4 * q4);
     const f32x4 keep = *reinterpret_cast<const f32x4*>(sKeep + 16 * w + 4 * q4);
 
@@ -402,7 +451,7 @@ __global__ __launch_bounds__(256) void k_delta_grads(GradArgs a) {
       f32x4 t1 = zero4(), t2 = zero4(), t3 = zero4();
 #pragma unroll
       for (int s = 0; s < VS; ++s) {
-        const int64_t at_row = (hc * DK + 16 * i + l16) * DV + 32 * s + 8 * q4;
+        const int64_t at_row = (hc * DK + state_row<ST>(i / ST, i % ST, l16)) * DV + 32 * s + 8 * q4;
         const f32x8 st = load_f32x8(a.states + at_row), ds = load_f32x8(a.dstates + at_row);
         if ((i & 3) == w) {
 #pragma unroll
@@ -423,7 +472,7 @@ __global__ __launch_bounds__(256) void k_delta_grads(GradArgs a) {
       dk[i] += t2 + t3;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int e = (16 * w + 4 * q4 + r) * kRow + 16 * i + l16;
+        const int e = (16 * w + 4 * q4 + r) * kRow + state_row<ST>(i / ST, i % ST, l16);
         const float kv = bf(sK[e]);
         s0[r] = fmaf(bf(sQ[e]), t1[r], fmaf(kv, t2[r], s0[r]));
         s1[r] = fmaf(kv, t3[r], s1[r]);
@@ -436,7 +485,7 @@ __global__ __launch_bounds__(256) void k_delta_grads(GradArgs a) {
     }
     dot = sum_rows(sum16(dot));
     if (lane == 0) sDot[w] = dot;
-    __syncthreads();
+    lds_barrier();
 
     // products within the chunk
 #pragma unroll
@@ -480,7 +529,7 @@ __global__ __launch_bounds__(256) void k_delta_grads(GradArgs a) {
       }
       sAcc[w][lane] = acc;
     }
-    __syncthreads();
+    lds_barrier();
     if (w == 0) {
       // sums of s over i >= t and of e over j < t
       float v0 = sS0[lane], v1 = sS1[lane];
@@ -519,7 +568,7 @@ __global__ __launch_bounds__(256) void k_delta_grads(GradArgs a) {
     for (int r = 0; r < 4; ++r) {
       const int64_t p = p0 + 16 * w + 4 * q4 + r;
       if (p < L) {
-        const int64_t to = ((b * L + a.sh.token(p)) * a.sh.hk + kh) * DK + 16 * i + l16;
+        const int64_t to = ((b * L + a.sh.token(p)) * a.sh.hk + kh) * DK + state_row<ST>(i / ST, i % ST, l16);
         bf16_t o;
         from_f32(dq[i][r], &o);
         a.dq[to] = o.bits;
@@ -543,7 +592,7 @@ __global__ __launch_bounds__(256) void k_delta_reduce(const float* part, float* 
   x = sum_rows(sum16(x));
   y = sum_rows(sum16(y));
   if (lane == 0) s[0][w] = x, s[1][w] = y;
-  __syncthreads();
+  lds_barrier();
   if (threadIdx.x != 0) return;
   dA[h] = (s[0][0] + s[0][1]) + (s[0][2] + s[0][3]);
   if (ddt_bias) ddt_bias[h] = (s[1][0] + s[1][1]) + (s[1][2] + s[1][3]);
@@ -553,8 +602,8 @@ template <int DK>
 void launch_rwalk(const RWalkArgs& a, int tiles, hipStream_t stream) {
   const int64_t rows = (a.batch * a.sh.heads + 7) / 8 * 8;
   const dim3 grid(static_cast<unsigned>(rows * (a.dv / (16 * tiles))));
-  if (tiles == 1) hipLaunchKernelGGL((k_delta_rwalk<DK, 1>), grid, dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((k_delta_rwalk<DK, 2>), grid, dim3(256), 0, stream, a);
+  if (tiles == 1) hipLaunchKernelGGL((k_delta_rwalk<DK, 1>), grid, dim3(512), 0, stream, a);
+  else hipLaunchKernelGGL((k_delta_rwalk<DK, 2>), grid, dim3(512), 0, stream, a);
 }
 
 template <int DK>

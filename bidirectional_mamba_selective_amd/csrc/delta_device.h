@@ -11,8 +11,12 @@
 namespace bimamba {
 namespace delta {
 
+constexpr int C = static_cast<int>(kC);
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -36,22 +40,42 @@ __device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float(static_
 
 // An fp32 value as a sum of bf16 parts, each the rounding of what the ones before leave: two parts carry it to 2^-17
 // relative, three to its last bit (where the parts stay normal numbers).
+// Two values as one part, which they lose: the rounded pair, first in the low half.
+__device__ __forceinline__ uint32_t take_part(float& a, float& b, bool more) {
+  const uint32_t p = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+  if (more) {
+    a -= __uint_as_float(p << 16);
+    b -= __uint_as_float(p & 0xffff0000u);
+  }
+  return p;
+}
+
 template <int PARTS>
 __device__ __forceinline__ void split4(f32x4 v, u32x2 (&p)[PARTS]) {
+  float a = v[0], b = v[1], c = v[2], d = v[3];
 #pragma unroll
-  for (int i = 0; i < PARTS; ++i) {
-    const bf16x4 r = __builtin_convertvector(v, bf16x4);
-    p[i] = __builtin_bit_cast(u32x2, r);
-    if (i + 1 < PARTS) v -= __builtin_convertvector(r, f32x4);
-  }
+  for (int i = 0; i < PARTS; ++i) p[i] = u32x2{take_part(a, b, i + 1 < PARTS), take_part(c, d, i + 1 < PARTS)};
 }
 
 template <int PARTS>
 __device__ __forceinline__ void split8(f32x8 v, bf16x8 (&p)[PARTS]) {
+  u32x2 lo[PARTS], hi[PARTS];
+  split4(f32x4{v[0], v[1], v[2], v[3]}, lo);
+  split4(f32x4{v[4], v[5], v[6], v[7]}, hi);
 #pragma unroll
-  for (int i = 0; i < PARTS; ++i) {
-    p[i] = __builtin_convertvector(v, bf16x8);
-    if (i + 1 < PARTS) v -= __builtin_convertvector(p[i], f32x8);
+  for (int i = 0; i < PARTS; ++i) p[i] = __builtin_bit_cast(bf16x8, u32x4{lo[i][0], lo[i][1], hi[i][0], hi[i][1]});
+}
+
+// A wavefront's rows of the state, column tile nt, as operands of three parts.
+template <int ST, int NT, typename T>
+__device__ __forceinline__ void split_own(const f32x4 (&S)[ST][NT], int nt, T (&p)[3]) {
+  u32x2 x[ST][3];
+#pragma unroll
+  for (int st = 0; st < ST; ++st) split4(S[st][nt], x[st]);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    if constexpr (ST == 1) p[i] = __builtin_bit_cast(T, x[0][i]);
+    else p[i] = __builtin_bit_cast(T, u32x4{x[0][i][0], x[0][i][1], x[1][i][0], x[1][i][1]});
   }
 }
 
@@ -72,6 +96,41 @@ __device__ __forceinline__ bf16x8 read8(const uint16_t* s, int row, int col) {
 template <int W>
 __device__ __forceinline__ void write4(uint16_t* s, int row, int col, u32x2 v) {
   *reinterpret_cast<u32x2*>(s + at<W>(row, col)) = v;
+}
+
+// D += A B with the terms that a wavefront's own result rows make up: lane l holds 4 (16 x 16 x 16) or 8 (16 x 16 x 32)
+// consecutive ones from 4 (l / 16) or 8 (l / 16).
+__device__ __forceinline__ f32x4 mfma_own(const bf16x8& a, const bf16x8& b, const f32x4& c) { return mfma(a, b, c); }
+__device__ __forceinline__ f32x4 mfma_own(const bf16x4& a, const bf16x4& b, const f32x4& c) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, a), __builtin_bit_cast(s16x4, b), c, 0, 0, 0);
+}
+
+template <int ST>
+struct Own;  // the operand of a wavefront's ST tiles of state rows
+template <>
+struct Own<1> {
+  typedef bf16x4 type;
+};
+template <>
+struct Own<2> {
+  typedef bf16x8 type;
+};
+
+// Rows of the state: a wavefront owns 16 ST consecutive ones as ST result tiles, whose rows are numbered so that a lane's
+// 4 ST values are consecutive rows (and make up an operand of the next product without leaving the lane): row m of tile t
+// of wavefront w is state row
+template <int ST>
+__device__ __forceinline__ int state_row(int w, int t, int m) {
+  return 16 * ST * w + 4 * ST * (m >> 2) + 4 * t + (m & 3);
+}
+
+// A barrier for what passes through LDS only: __syncthreads would also wait for every global load and store in flight, and
+// with it for the next chunk's operands.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // Where the operands of a triangular 64 x 64 matrix lie in a record.  lower: rows 16 w, k 32 s, entries with k <= row;
@@ -112,6 +171,82 @@ struct Shape {
   int rev;
   __device__ __forceinline__ int64_t token(int64_t p) const { return rev ? L - 1 - p : p; }
 };
+
+// The rows that a chunk's tokens have in a tensor [batch, L, nh, D] of bf16, one head, as a buffer: a token past either end
+// of the sequence lies outside of it, reads zeros and drops stores, and the address of every access is a lane's constant
+// (row_offset) plus `shift`.
+struct Rows {
+  __amdgpu_buffer_rsrc_t r;
+  int shift;  // bytes; not zero only where the reverse direction's last chunk would begin before the sequence
+};
+
+// base: the sequence's first row; pitch: bytes from one token's row to the next; width: bytes of a row that are used.
+__device__ __forceinline__ Rows chunk_rows(const void* base, const Shape& sh, int pitch, int width, int p0) {
+  int first = sh.rev ? static_cast<int>(sh.L) - C - p0 : p0;  // the chunk's lowest token
+  const int before = first < 0 ? first : 0;                   // (reverse) tokens that it would begin too early
+  const int left = static_cast<int>(sh.L) - first;
+  first -= before;
+  const int n = left < C ? left : C;
+  return Rows{__builtin_amdgcn_make_buffer_rsrc(
+                  const_cast<char*>(static_cast<const char*>(base) + static_cast<int64_t>(first) * pitch),
+                  static_cast<short>(0), (n + before) * pitch - pitch + width, 0x00020000),
+              before * pitch};
+}
+
+// Bytes from a chunk's lowest token to its i-th in the direction's order.
+__device__ __forceinline__ int row_offset(const Shape& sh, int pitch, int i) { return (sh.rev ? C - 1 - i : i) * pitch; }
+
+__device__ __forceinline__ bf16x8 row_load8(const Rows& t, int offset) {
+  return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(t.r, offset + t.shift, 0, 0));
+}
+
+__device__ __forceinline__ bf16x4 row_load4(const Rows& t, int offset) {
+  return __builtin_bit_cast(bf16x4, __builtin_amdgcn_raw_buffer_load_b64(t.r, offset + t.shift, 0, 0));
+}
+
+__device__ __forceinline__ void row_load(const Rows& t, int offset, bf16x8* v) { *v = row_load8(t, offset); }
+__device__ __forceinline__ void row_load(const Rows& t, int offset, bf16x4* v) { *v = row_load4(t, offset); }
+
+__device__ __forceinline__ uint16_t row_load1(const Rows& t, int offset) {
+  return __builtin_amdgcn_raw_buffer_load_b16(t.r, offset + t.shift, 0, 0);
+}
+
+__device__ __forceinline__ void row_store1(const Rows& t, int offset, float v) {
+  bf16_t o;
+  from_f32(v, &o);
+  __builtin_amdgcn_raw_buffer_store_b16(o.bits, t.r, offset + t.shift, 0, 0);
+}
+
+// A record of operands, the same way.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t record(const unsigned char* p, size_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<unsigned char*>(p), static_cast<short>(0),
+                                           static_cast<int>(bytes), 0x00020000);
+}
+
+// The frag-th operand from byte off (the same for all lanes) of a record; four share one scalar offset.
+__device__ __forceinline__ bf16x8 record_frag(__amdgpu_buffer_rsrc_t r, int off, int frag, int lane16) {
+  constexpr int kB = static_cast<int>(kFragBytes);
+  return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(r, lane16 + frag % 4 * kB,
+                                                                          off + frag / 4 * (4 * kB), 0));
+}
+
+// (x[0] + x[1] + x[2]) (y[0] + y[1] + y[2]) in three sums that do not wait for one another.
+__device__ __forceinline__ void mfma_three(const bf16x8 (&x)[3], const bf16x8 (&y)[3], f32x4 (&c)[3]) {
+  c[0] = mfma(x[0], y[2], c[0]);
+  c[1] = mfma(x[1], y[1], c[1]);
+  c[2] = mfma(x[2], y[0], c[2]);
+  c[1] = mfma(x[0], y[1], c[1]);
+  c[2] = mfma(x[1], y[0], c[2]);
+  c[0] = mfma(x[0], y[0], c[0]);
+}
+
+// x (y[0] + y[1] + y[2]), likewise.
+__device__ __forceinline__ void mfma_three(const bf16x8& x, const bf16x8 (&y)[3], f32x4 (&c)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) c[i] = mfma(x, y[i], c[i]);
+}
+
+__device__ __forceinline__ f32x4 sum3(const f32x4 (&c)[3]) { return c[0] + (c[1] + c[2]); }
 
 }  // namespace delta
 }  // namespace bimamba

@@ -24,7 +24,6 @@ namespace bimamba {
 namespace delta {
 namespace {
 
-constexpr int C = static_cast<int>(kC);
 constexpr int kPitch = C + 1;  // fp32 rows in LDS
 
 struct PrepArgs {
@@ -62,7 +61,7 @@ __device__ __forceinline__ f32x4 tile_product(const float* x, int row0, int k0, 
 // it to 2^-48 (differences of g stay exact to fp32 however far the chunk has decayed), beta; 64 of each.
 template <int DK, bool GRAD>
 __global__ __launch_bounds__(256) void k_delta_prep(PrepArgs a) {
-  constexpr int KS = DK / 32;
+  constexpr int KS = DK / 32, ST = DK / 64;
   constexpr int kRow = DK + 8;
   __shared__ float sN[C * kPitch], sT[C * kPitch], sA[C * kPitch];
   __shared__ float sHi[C], sLo[C], sBeta[C];
@@ -113,7 +112,7 @@ __global__ __launch_bounds__(256) void k_delta_prep(PrepArgs a) {
       *reinterpret_cast<bf16x8*>(sK + (16 * w + l16) * kRow + 32 * s + 8 * q4) = kf[s];
     }
   }
-  __syncthreads();
+  lds_barrier();
 
   // scores of this wavefront's 16 rows against the tokens up to them
   for (int j = 0; j <= w; ++j) {
@@ -135,7 +134,7 @@ __global__ __launch_bounds__(256) void k_delta_prep(PrepArgs a) {
     put_tile(sN, 16 * w, 16 * j, l16, q4, kk);
     put_tile(sA, 16 * w, 16 * j, l16, q4, qk);
   }
-  __syncthreads();
+  lds_barrier();
 
   // (I + N)^-1: the four 16 x 16 blocks on the diagonal by substitution, a column per lane, then blocks joined two by
   // two, [[x, 0], [n, y]]^-1 = [[x', 0], [-y' n x', y']], as stable as the substitution.  What is above the diagonal of
@@ -152,25 +151,25 @@ __global__ __launch_bounds__(256) void k_delta_prep(PrepArgs a) {
       sT[(o + i) * kPitch + o + l16] = v;
     }
   }
-  __syncthreads();
+  lds_barrier();
   if (w < 2) put_tile(sT, 32 * w, 32 * w + 16, l16, q4, tile_product<1>(sN, 32 * w + 16, 32 * w, sT, 32 * w, 32 * w, l16, q4));
-  __syncthreads();
+  lds_barrier();
   if (w < 2)
     put_tile(sT, 32 * w + 16, 32 * w, l16, q4,
              -tile_product<1>(sT, 32 * w + 16, 32 * w + 16, sT, 32 * w, 32 * w + 16, l16, q4));
-  __syncthreads();
+  lds_barrier();
   // the upper right block of each half is scratch until now and zero from here on, for the products over 32 terms
   if (w < 2) put_tile(sT, 32 * w, 32 * w + 16, l16, q4, zero4());
-  __syncthreads();
+  lds_barrier();
   {
     const int wr = 16 * (w >> 1), wc = 16 * (w & 1);
     const f32x4 x = tile_product<2>(sN, 32 + wr, 0, sT, 0, wc, l16, q4);
     put_tile(sT, wr, 32 + wc, l16, q4, x);
-    __syncthreads();
+    lds_barrier();
     const f32x4 y = tile_product<2>(sT, 32 + wr, 32, sT, 0, 32 + wc, l16, q4);
     put_tile(sT, 32 + wr, wc, l16, q4, -y);
   }
-  __syncthreads();
+  lds_barrier();
 
   // operands of the walk
 #pragma unroll
@@ -223,19 +222,20 @@ __global__ __launch_bounds__(256) void k_delta_prep(PrepArgs a) {
 #pragma unroll
   for (int which = 0; which < (GRAD ? 2 : 1); ++which) {
     if (which == 1) {
-      __syncthreads();
+      lds_barrier();
 #pragma unroll
       for (int s = 0; s < KS; ++s)
         *reinterpret_cast<bf16x8*>(sK + (16 * w + l16) * kRow + 32 * s + 8 * q4) = qf[s];
-      __syncthreads();
+      lds_barrier();
     }
-    for (int f = w; f < DK / 8; f += 4) {  // rows 16 (f / 2) of the transpose, tokens 32 (f % 2)
+    for (int f = w; f < DK / 8; f += 4) {  // tile f / 2 of the state's rows, tokens 32 (f % 2)
+      const int col = state_row<ST>(f / (2 * ST), f / 2 % ST, l16);
       union {
         uint16_t u[8];
         bf16x8 v;
       } x;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x.u[e] = sK[(32 * (f & 1) + 8 * q4 + e) * kRow + 16 * (f >> 1) + l16];
+      for (int e = 0; e < 8; ++e) x.u[e] = sK[(32 * (f & 1) + 8 * q4 + e) * kRow + col];
       store_frag(key, which * (DK / 8) + f, lane, x.v);
     }
   }
@@ -267,149 +267,218 @@ __device__ __forceinline__ bool place(int64_t slices, int64_t rows, int64_t* row
   return *row < rows;
 }
 
-// One workgroup: 16 NT columns of one head's state over `chunks` chunks.  Wavefront w owns the chunk's tokens 16 w .. + 15
-// and a quarter of the state's rows.  Per chunk three products follow from one another (K S, T R, K^T U), each through LDS
-// for the next one's operand, with one barrier before each.  The next chunk's operands are loaded into the registers of the current
-// chunk's as soon as these have been used.
+// One workgroup: 16 NT columns of one head's state over `chunks` chunks.  Four wavefronts carry the state, a quarter of its
+// rows each; three products follow from one another with one barrier before each:
+//   K S: every wavefront takes its own rows of S, which its registers hold in operand order, for all 64 tokens; the four
+//        partial sums meet in LDS, where wavefront w takes the sum for its tokens 16 w .. + 15
+//   T R: through LDS, rows 16 w .. + 15 of U
+//   K^T U: through LDS, the wavefront's rows of S
+// Four more take the products that only the output needs (Q S, A U) between the same barriers; without an output (SAVE)
+// there are none.  The next chunk's operands are loaded into the registers of the current chunk's as soon as these have
+// been used.
 template <int DK, int NT, bool SAVE>
-__global__ __launch_bounds__(256) void k_delta_walk(WalkArgs a) {
-  constexpr int KS = DK / 32, ST = DK / 64, NS = 16 * NT;
-  __shared__ __align__(16) uint16_t sS[3][NS * DK], sR[3][NS * C], sU[3][NS * C], sV[2][NS * C];
-  const int lane = threadIdx.x & 63, l16 = lane & 15, q4 = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+__global__ __launch_bounds__(SAVE ? 256 : 512, SAVE ? 1 : 2) void k_delta_walk(WalkArgs a) {
+  constexpr int KS = DK / 32, ST = DK / 64, NS = 16 * NT, kB = static_cast<int>(kFragBytes);
+  typedef typename Own<ST>::type own_t;
+  __shared__ __align__(16) float sP[NT][4][4][256];
+  __shared__ __align__(16) uint16_t sS[2][NS * DK], sR[3][NS * C], sU[3][NS * C], sV[2][NS * C];
+  const int lane = threadIdx.x & 63, l16 = lane & 15, q4 = lane >> 4, lane16 = lane * 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave & 3;
   int64_t bh, slice;
   if (!place(a.dv / NS, a.batch * a.sh.heads, &bh, &slice)) return;
   const int64_t b = bh / a.sh.heads, h = bh % a.sh.heads, kh = h / (a.sh.heads / a.sh.hk);
-  const int64_t L = a.sh.L, n0 = slice * NS;
+  const int n0 = static_cast<int>(slice) * NS, dv = static_cast<int>(a.dv);
+  const int chunks = static_cast<int>(a.chunks), first = static_cast<int>(a.chunk0) * C;
   const unsigned char* rec = a.heads + bh * a.seg * a.lay.bytes;
-  const unsigned char* key = a.keys + (b * a.sh.hk + kh) * a.seg * a.lay.key_bytes;
+  const int rec_bytes = static_cast<int>(a.lay.bytes);
+  const int key_pitch = static_cast<int>(a.sh.hk) * DK * 2, val_pitch = static_cast<int>(a.sh.heads) * dv * 2;
+  int val_row[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) val_row[r] = row_offset(a.sh, val_pitch, 16 * w + 4 * q4 + r) + 2 * l16;
+  auto gates4 = [&](__amdgpu_buffer_rsrc_t r, int row) {
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, 16 * q4, 4 * C * row + 64 * w, 0));
+  };
 
+  if (!SAVE && wave >= 4) {
+    const uint16_t* q0 = a.q + (b * a.sh.L * a.sh.hk + kh) * DK;
+    uint16_t* out0 = a.out + (b * a.sh.L * a.sh.heads + h) * dv + n0;
+    const int key_row = row_offset(a.sh, key_pitch, 16 * w + l16) + 16 * q4;
+    bf16x8 qf[KS], af[2][2];
+    f32x4 eg;
+    auto load_q = [&](int ci) {
+      const Rows q = chunk_rows(q0, a.sh, key_pitch, DK * 2, first + ci * C);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) qf[s] = row_load8(q, key_row + 64 * s);
+    };
+    auto load_a = [&](int ci) {
+      const __amdgpu_buffer_rsrc_t r = record(rec + static_cast<int64_t>(ci) * rec_bytes, a.lay.bytes);
+      eg = gates4(r, 0);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (lower_has(w, s))
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            af[s][i] = record_frag(r, static_cast<int>(a.lay.a) + lower_at(w, s) * 2 * kB, i, lane16);
+    };
+    load_q(0), load_a(0);
+    for (int ci = 0; ci < chunks; ++ci) {
+      const int next = ci + 1 < chunks ? ci + 1 : ci;
+      lds_barrier();
+      f32x4 o[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        o[nt][0] = o[nt][1] = zero4();
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            o[nt][i] = mfma(qf[s], read8<DK>(sS[i], 16 * nt + l16, 32 * s + 8 * q4), o[nt][i]);
+      }
+      load_q(next);
+      lds_barrier();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) o[nt][0] = (o[nt][0] + o[nt][1]) * (eg * a.scale);
+      lds_barrier();
+      const Rows out = chunk_rows(out0, a.sh, val_pitch, 2 * NS, first + ci * C);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        f32x4 low = zero4();
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          if (lower_has(w, s)) {
+            const bf16x8 hi = read8<C>(sV[0], 16 * nt + l16, 32 * s + 8 * q4);
+            const bf16x8 lo = read8<C>(sV[1], 16 * nt + l16, 32 * s + 8 * q4);
+            low = mfma(af[s][1], hi, low);
+            o[nt][0] = mfma(af[s][0], hi, o[nt][0]);
+            low = mfma(af[s][0], lo, low);
+          }
+        o[nt][0] += low;
+      }
+      load_a(next);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) row_store1(out, val_row[r] + 32 * nt, o[nt][0][r]);
+    }
+    return;
+  }
+
+  const uint16_t* k0 = a.k + (b * a.sh.L * a.sh.hk + kh) * DK + 16 * ST * w;
+  const uint16_t* v0 = a.v + (b * a.sh.L * a.sh.heads + h) * dv + n0;
+  const unsigned char* key = a.keys + (b * a.sh.hk + kh) * a.seg * a.lay.key_bytes;
+  const int key_bytes = static_cast<int>(a.lay.key_bytes);
+  // this lane's rows of the state: state_row(w, st, 4 q4 + r) = the first one + 4 st + r
+  const int64_t state0 = (bh * DK + state_row<ST>(w, 0, 4 * q4)) * dv + n0 + l16;
   f32x4 S[ST][NT];
 #pragma unroll
   for (int st = 0; st < ST; ++st)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t i = (bh * DK + 16 * (ST * w + st) + 4 * q4 + r) * a.dv + n0 + 16 * nt + l16;
-        S[st][nt][r] = a.state_in ? a.state_in[i] : 0.0f;
-      }
+      for (int r = 0; r < 4; ++r) S[st][nt][r] = a.state_in ? a.state_in[state0 + (4 * st + r) * dv + 16 * nt] : 0.0f;
 
-  bf16x8 kf[KS], qf[KS], tf[2][3], af[2][2], ktf[ST][2];
+  own_t kf[4];
+  bf16x8 tf[2][3], ktf[ST][2];
   uint16_t vv[NT][4];
   f32x4 eg, keep;
   float last;
-  auto load_rows = [&](int64_t ci, const uint16_t* src, bf16x8(&f)[KS]) {
-    const int64_t p = (a.chunk0 + ci) * C + 16 * w + l16;
-    const uint16_t* row = src + ((b * L + a.sh.token(p < L ? p : L - 1)) * a.sh.hk + kh) * DK + 8 * q4;
+  int key_row[4];
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      f[s] = *reinterpret_cast<const bf16x8*>(row + 32 * s);
-      if (p >= L) f[s] = zero8();
-    }
+  for (int i = 0; i < 4; ++i) key_row[i] = row_offset(a.sh, key_pitch, 16 * i + l16) + 8 * ST * q4;
+  auto load_rows = [&](int ci) {
+    const Rows k = chunk_rows(k0, a.sh, key_pitch, 32 * ST, first + ci * C);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) row_load(k, key_row[i], &kf[i]);
   };
-  auto load_v = [&](int64_t ci) {
+  auto load_v = [&](int ci) {
+    const Rows v = chunk_rows(v0, a.sh, val_pitch, 2 * NS, first + ci * C);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t p = (a.chunk0 + ci) * C + 16 * w + 4 * q4 + r;
-      const uint16_t* row = a.v + ((b * L + a.sh.token(p < L ? p : L - 1)) * a.sh.heads + h) * a.dv + n0 + l16;
+    for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) vv[nt][r] = p < L ? row[16 * nt] : static_cast<uint16_t>(0);
-    }
+      for (int nt = 0; nt < NT; ++nt) vv[nt][r] = row_load1(v, val_row[r] + 32 * nt);
   };
-  auto load_t = [&](int64_t ci) {
+  auto load_t = [&](int ci) {
+    const __amdgpu_buffer_rsrc_t r = record(rec + static_cast<int64_t>(ci) * rec_bytes, a.lay.bytes);
 #pragma unroll
     for (int s = 0; s < 2; ++s)
       if (lower_has(w, s))
 #pragma unroll
-        for (int i = 0; i < 3; ++i) tf[s][i] = load_frag(rec + ci * a.lay.bytes + a.lay.t, lower_at(w, s) * 3 + i, lane);
+        for (int i = 0; i < 3; ++i)
+          tf[s][i] = record_frag(r, static_cast<int>(a.lay.t) + lower_at(w, s) * 3 * kB, i, lane16);
   };
-  auto load_a = [&](int64_t ci) {
-    if constexpr (!SAVE) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (lower_has(w, s))
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            af[s][i] = load_frag(rec + ci * a.lay.bytes + a.lay.a, lower_at(w, s) * 2 + i, lane);
-    }
+  auto load_gates = [&](int ci) {
+    const __amdgpu_buffer_rsrc_t r = record(rec + static_cast<int64_t>(ci) * rec_bytes, a.lay.bytes);
+    eg = gates4(r, 0);
+    keep = gates4(r, 1);
+    last = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, 4 * (C - 1), 0, 0));
   };
-  auto load_kt = [&](int64_t ci) {
+  auto load_kt = [&](int ci) {
+    const __amdgpu_buffer_rsrc_t r = record(key + static_cast<int64_t>(ci) * key_bytes, a.lay.key_bytes);
 #pragma unroll
     for (int st = 0; st < ST; ++st)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) ktf[st][s] = load_frag(key + ci * a.lay.key_bytes, (ST * w + st) * 2 + s, lane);
+      for (int s = 0; s < 2; ++s) ktf[st][s] = record_frag(r, ST * w * 2 * kB, 2 * st + s, lane16);
   };
-  auto load_gates = [&](int64_t ci) {
-    const float* g = reinterpret_cast<const float*>(rec + ci * a.lay.bytes);
-    eg = *reinterpret_cast<const f32x4*>(g + 16 * w + 4 * q4);
-    keep = *reinterpret_cast<const f32x4*>(g + C + 16 * w + 4 * q4);
-    last = g[C - 1];
-  };
-  load_rows(0, a.k, kf);
-  if constexpr (!SAVE) load_rows(0, a.q, qf);
-  load_v(0), load_t(0), load_a(0), load_kt(0), load_gates(0);
+  load_rows(0), load_v(0), load_t(0), load_gates(0), load_kt(0);
 
-  for (int64_t ci = 0; ci < a.chunks; ++ci) {
-    const int64_t next = ci + 1 < a.chunks ? ci + 1 : ci;
-#pragma unroll
-    for (int st = 0; st < ST; ++st)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        u32x2 p[3];
-        split4(S[st][nt], p);
-#pragma unroll
-        for (int i = 0; i < 3; ++i) write4<DK>(sS[i], 16 * nt + l16, 16 * (ST * w + st) + 4 * q4, p[i]);
-        if constexpr (SAVE) {
-          float* to = a.states + ((bh * a.seg + ci) * DK + 16 * (ST * w + st) + 4 * q4) * a.dv + n0 + 16 * nt + l16;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) to[r * a.dv] = S[st][nt][r];
-        }
-      }
-    __syncthreads();
-    f32x4 P[NT], O[NT];
+  for (int ci = 0; ci < chunks; ++ci) {
+    const int next = ci + 1 < chunks ? ci + 1 : ci;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      P[nt] = O[nt] = zero4();
+      own_t own[3];
+      split_own<ST, NT>(S, nt, own);
+      f32x4 P[4];
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const bf16x8 x[1] = {kf[s]};
-        bf16x8 y[3];
+      for (int i = 0; i < 4; ++i) P[i] = zero4();
 #pragma unroll
-        for (int i = 0; i < 3; ++i) y[i] = read8<DK>(sS[i], 16 * nt + l16, 32 * s + 8 * q4);
-        P[nt] = mfma_parts(x, y, P[nt]);
-        if constexpr (!SAVE) {
-          O[nt] = mfma(qf[s], y[1], O[nt]);
-          O[nt] = mfma(qf[s], y[0], O[nt]);
-        }
+      for (int j = 2; j >= 0; --j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) P[i] = mfma_own(kf[i], own[j], P[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4*>(&sP[nt][w][i][4 * lane]) = P[i];
+      if constexpr (SAVE) {
+        float* to = a.states + ((bh * a.seg + ci) * DK + state_row<ST>(w, 0, 4 * q4)) * dv + n0 + 16 * nt + l16;
+#pragma unroll
+        for (int st = 0; st < ST; ++st)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) to[(4 * st + r) * dv] = S[st][nt][r];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<own_t*>(sS[i] + at<DK>(16 * nt + l16, state_row<ST>(w, 0, 4 * q4))) = own[i];
       }
     }
-    load_rows(next, a.k, kf);
-    if constexpr (!SAVE) load_rows(next, a.q, qf);
+    load_rows(next);
+    lds_barrier();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      f32x4 p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const f32x4*>(&sP[nt][i][w][4 * lane]);
+      const f32x4 ks = (p[0] + p[1]) + (p[2] + p[3]);
       f32x4 R;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) R[r] = fmaf(-eg[r], P[nt][r], bf(vv[nt][r]));
-      u32x2 p[3];
-      split4(R, p);
+      for (int r = 0; r < 4; ++r) R[r] = fmaf(-eg[r], ks[r], bf(vv[nt][r]));
+      u32x2 x[3];
+      split4(R, x);
 #pragma unroll
-      for (int i = 0; i < 3; ++i) write4<C>(sR[i], 16 * nt + l16, 16 * w + 4 * q4, p[i]);
+      for (int i = 0; i < 3; ++i) write4<C>(sR[i], 16 * nt + l16, 16 * w + 4 * q4, x[i]);
     }
     load_v(next);
-    __syncthreads();
+    lds_barrier();
     f32x4 U[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      U[nt] = zero4();
+      f32x4 u[3] = {zero4(), zero4(), zero4()};
 #pragma unroll
       for (int s = 0; s < 2; ++s)
         if (lower_has(w, s)) {
           bf16x8 y[3];
 #pragma unroll
           for (int i = 0; i < 3; ++i) y[i] = read8<C>(sR[i], 16 * nt + l16, 32 * s + 8 * q4);
-          U[nt] = mfma_parts(tf[s], y, U[nt]);
+          mfma_three(tf[s], y, u);
         }
+      U[nt] = sum3(u);
     }
     load_t(next);
 #pragma unroll
@@ -419,9 +488,9 @@ __global__ __launch_bounds__(256) void k_delta_walk(WalkArgs a) {
 #pragma unroll
       for (int i = 0; i < 3; ++i) write4<C>(sU[i], 16 * nt + l16, 16 * w + 4 * q4, p[i]);
       if constexpr (SAVE) {
-        float* to = a.us + ((bh * a.seg + ci) * C + 16 * w + 4 * q4) * a.dv + n0 + 16 * nt + l16;
+        float* to = a.us + ((bh * a.seg + ci) * C + 16 * w + 4 * q4) * dv + n0 + 16 * nt + l16;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) to[r * a.dv] = U[nt][r];
+        for (int r = 0; r < 4; ++r) to[r * dv] = U[nt][r];
       } else {
         u32x2 o[2];
         split4(U[nt], o);
@@ -429,44 +498,26 @@ __global__ __launch_bounds__(256) void k_delta_walk(WalkArgs a) {
         for (int i = 0; i < 2; ++i) write4<C>(sV[i], 16 * nt + l16, 16 * w + 4 * q4, o[i]);
       }
     }
-    __syncthreads();
+    const float decay = last;
+    load_gates(next);
+    lds_barrier();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      f32x4 add[ST][3];
 #pragma unroll
-      for (int st = 0; st < ST; ++st) S[st][nt] *= last;
+      for (int st = 0; st < ST; ++st) add[st][0] = add[st][1] = add[st][2] = zero4();
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         bf16x8 y[3];
 #pragma unroll
         for (int i = 0; i < 3; ++i) y[i] = read8<C>(sU[i], 16 * nt + l16, 32 * s + 8 * q4);
 #pragma unroll
-        for (int st = 0; st < ST; ++st) {
-          const bf16x8 x[1] = {ktf[st][s]};
-          S[st][nt] = mfma_parts(x, y, S[st][nt]);
-        }
+        for (int st = 0; st < ST; ++st) mfma_three(ktf[st][s], y, add[st]);
       }
-      if constexpr (!SAVE) {
-        O[nt] *= eg * a.scale;
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-          if (lower_has(w, s)) {
-            bf16x8 y[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) y[i] = read8<C>(sV[i], 16 * nt + l16, 32 * s + 8 * q4);
-            O[nt] = mfma_parts(af[s], y, O[nt]);
-          }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int64_t p = (a.chunk0 + ci) * C + 16 * w + 4 * q4 + r;
-          if (p < L) {
-            bf16_t o;
-            from_f32(O[nt][r], &o);
-            a.out[((b * L + a.sh.token(p)) * a.sh.heads + h) * a.dv + n0 + 16 * nt + l16] = o.bits;
-          }
-        }
-      }
+      for (int st = 0; st < ST; ++st) S[st][nt] = S[st][nt] * decay + sum3(add[st]);
     }
-    load_a(next), load_kt(next), load_gates(next);
+    load_kt(next);
   }
   if (a.state_out) {
 #pragma unroll
@@ -474,8 +525,7 @@ __global__ __launch_bounds__(256) void k_delta_walk(WalkArgs a) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          a.state_out[(bh * DK + 16 * (ST * w + st) + 4 * q4 + r) * a.dv + n0 + 16 * nt + l16] = S[st][nt][r];
+        for (int r = 0; r < 4; ++r) a.state_out[state0 + (4 * st + r) * dv + 16 * nt] = S[st][nt][r];
   }
 }
 
@@ -573,8 +623,8 @@ template <int DK, bool SAVE>
 void launch_walk(const WalkArgs& a, int tiles, hipStream_t stream) {
   const int64_t rows = (a.batch * a.sh.heads + 7) / 8 * 8;
   const dim3 grid(static_cast<unsigned>(rows * (a.dv / (16 * tiles))));
-  if (tiles == 1) hipLaunchKernelGGL((k_delta_walk<DK, 1, SAVE>), grid, dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((k_delta_walk<DK, 2, SAVE>), grid, dim3(256), 0, stream, a);
+  if (tiles == 1) hipLaunchKernelGGL((k_delta_walk<DK, 1, SAVE>), grid, dim3(SAVE ? 256 : 512), 0, stream, a);
+  else hipLaunchKernelGGL((k_delta_walk<DK, 2, SAVE>), grid, dim3(SAVE ? 256 : 512), 0, stream, a);
 }
 
 }  // namespace
