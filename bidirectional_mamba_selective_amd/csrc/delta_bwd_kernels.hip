@@ -69,7 +69,7 @@ __global__ __launch_bounds__(512, 2) void k_delta_rwalk(RWalkArgs a) {
   const int key_pitch = static_cast<int>(a.sh.hk) * DK * 2, val_pitch = static_cast<int>(a.sh.heads) * dv * 2;
   int val_row[4];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) val_row[r] = row_offset(a.sh, val_pitch, 16 * w + 4 * q4 + r) + 2 * l16;
+  for (int r = 0; r < 4; ++r) val_row[r] = a.sh.place(16 * w + 4 * q4 + r) * val_pitch + 2 * l16;
   auto gates4 = [&](__amdgpu_buffer_rsrc_t r, int row) {
     return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, 16 * q4, 4 * C * row + 64 * w, 0));
   };
@@ -97,7 +97,7 @@ __global__ __launch_bounds__(512, 2) void k_delta_rwalk(RWalkArgs a) {
     uint16_t vv[NT][4];
     f32x4 eg;
     auto load = [&](int ci) {
-      const Rows o = chunk_rows(o0, a.sh, val_pitch, 2 * NS, ci * C);
+      const __amdgpu_buffer_rsrc_t o = run_rows(o0, a.sh, val_pitch, 2 * NS, a.sh.run(ci, chunks));
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -175,9 +175,9 @@ __global__ __launch_bounds__(512, 2) void k_delta_rwalk(RWalkArgs a) {
   float last;
   int key_row[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) key_row[i] = row_offset(a.sh, key_pitch, 16 * i + l16) + 8 * ST * q4;
+  for (int i = 0; i < 4; ++i) key_row[i] = a.sh.place(16 * i + l16) * key_pitch + 8 * ST * q4;
   auto load_k = [&](int ci) {
-    const Rows k = chunk_rows(k0, a.sh, key_pitch, 32 * ST, ci * C);
+    const __amdgpu_buffer_rsrc_t k = run_rows(k0, a.sh, key_pitch, 32 * ST, a.sh.run(ci, chunks));
 #pragma unroll
     for (int i = 0; i < 4; ++i) row_load(k, key_row[i], &kf[i]);
   };
@@ -248,7 +248,7 @@ __global__ __launch_bounds__(512, 2) void k_delta_rwalk(RWalkArgs a) {
     const float decay = last;
     load_gates(next);
     lds_barrier();
-    const Rows out = chunk_rows(dv0, a.sh, val_pitch, 2 * NS, ci * C);
+    const __amdgpu_buffer_rsrc_t out = run_rows(dv0, a.sh, val_pitch, 2 * NS, a.sh.run(ci, chunks));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       f32x4 add[ST][3];
@@ -347,18 +347,18 @@ __global__ __launch_bounds__(256) void k_delta_grads(GradArgs a) {
   const int lane = threadIdx.x & 63, l16 = lane & 15, q4 = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t ci = blockIdx.x, kh = blockIdx.y, b = blockIdx.z, L = a.sh.L, share = a.sh.heads / a.sh.hk;
-  const int64_t p0 = ci * C;
+  const int64_t t0 = static_cast<int64_t>(a.sh.run(static_cast<int>(ci), static_cast<int>(a.chunks))) * C;
   const unsigned char* key = a.keys + ((b * a.sh.hk + kh) * a.chunks + ci) * a.lay.key_bytes;
 
   bf16x8 kf[KS], qf[KS];
   {
-    const int64_t p = p0 + 16 * w + l16;
-    const int64_t row = ((b * L + a.sh.token(p < L ? p : L - 1)) * a.sh.hk + kh) * DK + 8 * q4;
+    const int64_t t = t0 + a.sh.place(16 * w + l16);
+    const int64_t row = ((b * L + (t < L ? t : L - 1)) * a.sh.hk + kh) * DK + 8 * q4;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       kf[s] = *reinterpret_cast<const bf16x8*>(a.k + row + 32 * s);
       qf[s] = *reinterpret_cast<const bf16x8*>(a.q + row + 32 * s);
-      if (p >= L) kf[s] = qf[s] = zero8();
+      if (t >= L) kf[s] = qf[s] = zero8();
       *reinterpret_cast<bf16x8*>(sK + (16 * w + l16) * kRow + 32 * s + 8 * q4) = kf[s];
       *reinterpret_cast<bf16x8*>(sQ + (16 * w + l16) * kRow + 32 * s + 8 * q4) = qf[s];
     }
@@ -376,15 +376,15 @@ __global__ __launch_bounds__(256) void k_delta_grads(GradArgs a) {
     // this wavefront's rows of dO, dR and U as operands
     bf16x8 od[VS], rd[VS][2], ud[VS][2];
     {
-      const int64_t p = p0 + 16 * w + l16;
-      const uint16_t* row = a.dout + ((b * L + a.sh.token(p < L ? p : L - 1)) * a.sh.heads + h) * DV + 8 * q4;
+      const int64_t t = t0 + a.sh.place(16 * w + l16);
+      const uint16_t* row = a.dout + ((b * L + (t < L ? t : L - 1)) * a.sh.heads + h) * DV + 8 * q4;
       float dot = 0.0f;
       const float beta = gates[4 * C + 16 * w + l16];
       const float rb = beta > 1e-30f ? 1.0f / beta : 0.0f;
 #pragma unroll
       for (int s = 0; s < VS; ++s) {
         od[s] = *reinterpret_cast<const bf16x8*>(row + 32 * s);
-        if (p >= L) od[s] = zero8();
+        if (t >= L) od[s] = zero8();
         const f32x8 r = load_f32x8(a.drs + (hc * C + 16 * w + l16) * DV + 32 * s + 8 * q4);
         const f32x8 u = load_f32x8(a.us + (hc * C + 16 * w + l16) * DV + 32 * s + 8 * q4);
 #pragma unroll
@@ -543,10 +543,9 @@ __global__ __launch_bounds__(256) void k_delta_grads(GradArgs a) {
       const float last = sEg[C - 1];
       float dg = ((sAcc[0][lane] + sAcc[1][lane]) + (sAcc[2][lane] + sAcc[3][lane])) + v0 + (lane > 0 ? before : 0.0f);
       dg = fmaf(last, (sDot[0] + sDot[1]) + (sDot[2] + sDot[3]), dg);
-      const int64_t p = p0 + lane;
       float pa = 0.0f, pb = 0.0f;
-      if (p < L) {
-        const int64_t t = (b * L + a.sh.token(p)) * a.sh.heads + h;
+      if (t0 + a.sh.place(lane) < L) {
+        const int64_t t = (b * L + t0 + a.sh.place(lane)) * a.sh.heads + h;
         const float x = bf(a.dt[t]) + (a.dt_bias ? a.dt_bias[h] : 0.0f);
         const float ddt = dg * a.A[h] * sigmoid_f32(x);
         pa = dg * softplus_f32(x);
@@ -566,9 +565,9 @@ __global__ __launch_bounds__(256) void k_delta_grads(GradArgs a) {
   for (int i = 0; i < KT; ++i)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int64_t p = p0 + 16 * w + 4 * q4 + r;
-      if (p < L) {
-        const int64_t to = ((b * L + a.sh.token(p)) * a.sh.hk + kh) * DK + state_row<ST>(i / ST, i % ST, l16);
+      const int64_t t = t0 + a.sh.place(16 * w + 4 * q4 + r);
+      if (t < L) {
+        const int64_t to = ((b * L + t) * a.sh.hk + kh) * DK + state_row<ST>(i / ST, i % ST, l16);
         bf16_t o;
         from_f32(dq[i][r], &o);
         a.dq[to] = o.bits;

@@ -164,57 +164,48 @@ __device__ __forceinline__ float ex(float v) { return fast_exp2(v * kLog2e); }
 
 __device__ __forceinline__ float sigmoid_f32(float v) { return __builtin_amdgcn_rcpf(1.0f + ex(-v)); }
 
-// What a call works on; the sequence's tokens in the order in which the direction meets them: place p is token
-// p (forward) or L - 1 - p (reverse).
+// What a call works on.  Chunks are runs of 64 tokens from the sequence's start in both directions; the reverse one meets
+// them from the last to the first, and their tokens from the last to the first.  In the last run the places past the
+// sequence's end are empty (for the reverse direction the first ones that it meets): q = k = v = 0, no decay, beta = 0,
+// a token that changes nothing.
 struct Shape {
   int64_t L, hk, heads;
   int rev;
-  __device__ __forceinline__ int64_t token(int64_t p) const { return rev ? L - 1 - p : p; }
+  // the run that is met as the i-th of n, and the token of its i-th place
+  __device__ __forceinline__ int run(int i, int n) const { return rev ? n - 1 - i : i; }
+  __device__ __forceinline__ int place(int i) const { return rev ? C - 1 - i : i; }
 };
 
-// The rows that a chunk's tokens have in a tensor [batch, L, nh, D] of bf16, one head, as a buffer: a token past either end
-// of the sequence lies outside of it, reads zeros and drops stores, and the address of every access is a lane's constant
-// (row_offset) plus `shift`.
-struct Rows {
-  __amdgpu_buffer_rsrc_t r;
-  int shift;  // bytes; not zero only where the reverse direction's last chunk would begin before the sequence
-};
-
-// base: the sequence's first row; pitch: bytes from one token's row to the next; width: bytes of a row that are used.
-__device__ __forceinline__ Rows chunk_rows(const void* base, const Shape& sh, int pitch, int width, int p0) {
-  int first = sh.rev ? static_cast<int>(sh.L) - C - p0 : p0;  // the chunk's lowest token
-  const int before = first < 0 ? first : 0;                   // (reverse) tokens that it would begin too early
-  const int left = static_cast<int>(sh.L) - first;
-  first -= before;
-  const int n = left < C ? left : C;
-  return Rows{__builtin_amdgcn_make_buffer_rsrc(
-                  const_cast<char*>(static_cast<const char*>(base) + static_cast<int64_t>(first) * pitch),
-                  static_cast<short>(0), (n + before) * pitch - pitch + width, 0x00020000),
-              before * pitch};
+// The rows of a run of 64 tokens in a tensor [batch, L, nh, D] of bf16, one head, as a buffer: rows past the sequence's end
+// read zeros and drop stores, and a lane's offset is the same for every run.  base: the sequence's first row; pitch:
+// bytes from one token's row to the next; width: bytes of a row that are used.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t run_rows(const void* base, const Shape& sh, int pitch, int width,
+                                                           int run) {
+  const int left = static_cast<int>(sh.L) - run * C, n = left < C ? left : C;
+  return __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<char*>(static_cast<const char*>(base) + static_cast<int64_t>(run) * (C * pitch)),
+      static_cast<short>(0), (n - 1) * pitch + width, 0x00020000);
 }
 
-// Bytes from a chunk's lowest token to its i-th in the direction's order.
-__device__ __forceinline__ int row_offset(const Shape& sh, int pitch, int i) { return (sh.rev ? C - 1 - i : i) * pitch; }
-
-__device__ __forceinline__ bf16x8 row_load8(const Rows& t, int offset) {
-  return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(t.r, offset + t.shift, 0, 0));
+__device__ __forceinline__ bf16x8 row_load8(__amdgpu_buffer_rsrc_t t, int offset) {
+  return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(t, offset, 0, 0));
 }
 
-__device__ __forceinline__ bf16x4 row_load4(const Rows& t, int offset) {
-  return __builtin_bit_cast(bf16x4, __builtin_amdgcn_raw_buffer_load_b64(t.r, offset + t.shift, 0, 0));
+__device__ __forceinline__ bf16x4 row_load4(__amdgpu_buffer_rsrc_t t, int offset) {
+  return __builtin_bit_cast(bf16x4, __builtin_amdgcn_raw_buffer_load_b64(t, offset, 0, 0));
 }
 
-__device__ __forceinline__ void row_load(const Rows& t, int offset, bf16x8* v) { *v = row_load8(t, offset); }
-__device__ __forceinline__ void row_load(const Rows& t, int offset, bf16x4* v) { *v = row_load4(t, offset); }
+__device__ __forceinline__ void row_load(__amdgpu_buffer_rsrc_t t, int offset, bf16x8* v) { *v = row_load8(t, offset); }
+__device__ __forceinline__ void row_load(__amdgpu_buffer_rsrc_t t, int offset, bf16x4* v) { *v = row_load4(t, offset); }
 
-__device__ __forceinline__ uint16_t row_load1(const Rows& t, int offset) {
-  return __builtin_amdgcn_raw_buffer_load_b16(t.r, offset + t.shift, 0, 0);
+__device__ __forceinline__ uint16_t row_load1(__amdgpu_buffer_rsrc_t t, int offset) {
+  return __builtin_amdgcn_raw_buffer_load_b16(t, offset, 0, 0);
 }
 
-__device__ __forceinline__ void row_store1(const Rows& t, int offset, float v) {
+__device__ __forceinline__ void row_store1(__amdgpu_buffer_rsrc_t t, int offset, float v) {
   bf16_t o;
   from_f32(v, &o);
-  __builtin_amdgcn_raw_buffer_store_b16(o.bits, t.r, offset + t.shift, 0, 0);
+  __builtin_amdgcn_raw_buffer_store_b16(o.bits, t, offset, 0, 0);
 }
 
 // A record of operands, the same way.

@@ -37,7 +37,8 @@ struct PrepArgs {
   unsigned char* keys;   // K^T (and Q^T), [batch][key head][seg]
   Shape sh;
   Layout lay;
-  int64_t chunk0, seg;  // first chunk of the segment, records per head
+  int64_t chunk0, seg;  // the segment's first chunk in the direction's order, records per head
+  int chunks;           // of the whole sequence
   float scale;
 };
 
@@ -69,16 +70,15 @@ __global__ __launch_bounds__(256) void k_delta_prep(PrepArgs a) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, l16 = lane & 15, q4 = lane >> 4;
   const int64_t ci = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int64_t share = a.sh.heads / a.sh.hk, kh = h / share, L = a.sh.L;
-  const int64_t p0 = (a.chunk0 + ci) * C;
+  const int64_t t0 = static_cast<int64_t>(a.sh.run(static_cast<int>(a.chunk0 + ci), a.chunks)) * C;
   unsigned char* rec = a.heads + ((b * a.sh.heads + h) * a.seg + ci) * a.lay.bytes;
   float* gates = reinterpret_cast<float*>(rec);
 
-  // tokens past the end: q = k = 0, no decay, beta = 0; they change nothing
   if (w == 0) {
-    const int64_t p = p0 + lane;
+    const int64_t t = t0 + a.sh.place(lane);
     float g = 0.0f, beta = 0.0f;
-    if (p < L) {
-      const int64_t i = (b * L + a.sh.token(p)) * a.sh.heads + h;
+    if (t < L) {
+      const int64_t i = (b * L + t) * a.sh.heads + h;
       g = softplus_f32(bf(a.dt[i]) + (a.dt_bias ? a.dt_bias[h] : 0.0f)) * a.A[h];
       // e^-256 is 0 in fp32 as any stronger decay is; sums of the logarithms stay finite
       if (g < -256.0f) g = -256.0f;
@@ -102,13 +102,13 @@ __global__ __launch_bounds__(256) void k_delta_prep(PrepArgs a) {
   }
   bf16x8 kf[KS], qf[KS];
   {
-    const int64_t p = p0 + 16 * w + l16;
-    const int64_t row = ((b * L + a.sh.token(p < L ? p : L - 1)) * a.sh.hk + kh) * DK;
+    const int64_t t = t0 + a.sh.place(16 * w + l16);
+    const int64_t row = ((b * L + (t < L ? t : L - 1)) * a.sh.hk + kh) * DK;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       kf[s] = *reinterpret_cast<const bf16x8*>(a.k + row + 32 * s + 8 * q4);
       qf[s] = *reinterpret_cast<const bf16x8*>(a.q + row + 32 * s + 8 * q4);
-      if (p >= L) kf[s] = qf[s] = zero8();
+      if (t >= L) kf[s] = qf[s] = zero8();
       *reinterpret_cast<bf16x8*>(sK + (16 * w + l16) * kRow + 32 * s + 8 * q4) = kf[s];
     }
   }
@@ -254,7 +254,8 @@ struct WalkArgs {
   float* us;              // backward: U, [batch][head][chunk][64][dv]
   Shape sh;
   Layout lay;
-  int64_t batch, dv, chunk0, chunks, seg;
+  int64_t batch, dv, seg;
+  int first, chunks, all;  // the segment's first chunk, its chunks, those of the whole sequence
   float scale;
 };
 
@@ -288,13 +289,13 @@ __global__ __launch_bounds__(SAVE ? 256 : 512, SAVE ? 1 : 2) void k_delta_walk(W
   if (!place(a.dv / NS, a.batch * a.sh.heads, &bh, &slice)) return;
   const int64_t b = bh / a.sh.heads, h = bh % a.sh.heads, kh = h / (a.sh.heads / a.sh.hk);
   const int n0 = static_cast<int>(slice) * NS, dv = static_cast<int>(a.dv);
-  const int chunks = static_cast<int>(a.chunks), first = static_cast<int>(a.chunk0) * C;
+  const int chunks = a.chunks;
   const unsigned char* rec = a.heads + bh * a.seg * a.lay.bytes;
   const int rec_bytes = static_cast<int>(a.lay.bytes);
   const int key_pitch = static_cast<int>(a.sh.hk) * DK * 2, val_pitch = static_cast<int>(a.sh.heads) * dv * 2;
   int val_row[4];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) val_row[r] = row_offset(a.sh, val_pitch, 16 * w + 4 * q4 + r) + 2 * l16;
+  for (int r = 0; r < 4; ++r) val_row[r] = a.sh.place(16 * w + 4 * q4 + r) * val_pitch + 2 * l16;
   auto gates4 = [&](__amdgpu_buffer_rsrc_t r, int row) {
     return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, 16 * q4, 4 * C * row + 64 * w, 0));
   };
@@ -302,17 +303,17 @@ __global__ __launch_bounds__(SAVE ? 256 : 512, SAVE ? 1 : 2) void k_delta_walk(W
   if (!SAVE && wave >= 4) {
     const uint16_t* q0 = a.q + (b * a.sh.L * a.sh.hk + kh) * DK;
     uint16_t* out0 = a.out + (b * a.sh.L * a.sh.heads + h) * dv + n0;
-    const int key_row = row_offset(a.sh, key_pitch, 16 * w + l16) + 16 * q4;
+    const int key_row = a.sh.place(16 * w + l16) * key_pitch + 16 * q4;
     bf16x8 qf[KS], af[2][2];
     f32x4 eg;
     auto load_q = [&](int ci) {
-      const Rows q = chunk_rows(q0, a.sh, key_pitch, DK * 2, first + ci * C);
+      const __amdgpu_buffer_rsrc_t q = run_rows(q0, a.sh, key_pitch, DK * 2, a.sh.run(a.first + ci, a.all));
 #pragma unroll
       for (int s = 0; s < KS; ++s) qf[s] = row_load8(q, key_row + 64 * s);
     };
-    auto load_a = [&](int ci) {
-      const __amdgpu_buffer_rsrc_t r = record(rec + static_cast<int64_t>(ci) * rec_bytes, a.lay.bytes);
-      eg = gates4(r, 0);
+    auto load_eg = [&]() { eg = gates4(record(rec, a.lay.bytes), 0); };
+    auto load_a = [&]() {
+      const __amdgpu_buffer_rsrc_t r = record(rec, a.lay.bytes);
 #pragma unroll
       for (int s = 0; s < 2; ++s)
         if (lower_has(w, s))
@@ -320,7 +321,7 @@ __global__ __launch_bounds__(SAVE ? 256 : 512, SAVE ? 1 : 2) void k_delta_walk(W
           for (int i = 0; i < 2; ++i)
             af[s][i] = record_frag(r, static_cast<int>(a.lay.a) + lower_at(w, s) * 2 * kB, i, lane16);
     };
-    load_q(0), load_a(0);
+    load_q(0), load_eg(), load_a();
     for (int ci = 0; ci < chunks; ++ci) {
       const int next = ci + 1 < chunks ? ci + 1 : ci;
       lds_barrier();
@@ -338,8 +339,10 @@ __global__ __launch_bounds__(SAVE ? 256 : 512, SAVE ? 1 : 2) void k_delta_walk(W
       lds_barrier();
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) o[nt][0] = (o[nt][0] + o[nt][1]) * (eg * a.scale);
+      if (next > ci) rec += rec_bytes;
+      load_eg();
       lds_barrier();
-      const Rows out = chunk_rows(out0, a.sh, val_pitch, 2 * NS, first + ci * C);
+      const __amdgpu_buffer_rsrc_t out = run_rows(out0, a.sh, val_pitch, 2 * NS, a.sh.run(a.first + ci, a.all));
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         f32x4 low = zero4();
@@ -354,7 +357,7 @@ __global__ __launch_bounds__(SAVE ? 256 : 512, SAVE ? 1 : 2) void k_delta_walk(W
           }
         o[nt][0] += low;
       }
-      load_a(next);
+      load_a();
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -384,21 +387,21 @@ __global__ __launch_bounds__(SAVE ? 256 : 512, SAVE ? 1 : 2) void k_delta_walk(W
   float last;
   int key_row[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) key_row[i] = row_offset(a.sh, key_pitch, 16 * i + l16) + 8 * ST * q4;
+  for (int i = 0; i < 4; ++i) key_row[i] = a.sh.place(16 * i + l16) * key_pitch + 8 * ST * q4;
   auto load_rows = [&](int ci) {
-    const Rows k = chunk_rows(k0, a.sh, key_pitch, 32 * ST, first + ci * C);
+    const __amdgpu_buffer_rsrc_t k = run_rows(k0, a.sh, key_pitch, 32 * ST, a.sh.run(a.first + ci, a.all));
 #pragma unroll
     for (int i = 0; i < 4; ++i) row_load(k, key_row[i], &kf[i]);
   };
   auto load_v = [&](int ci) {
-    const Rows v = chunk_rows(v0, a.sh, val_pitch, 2 * NS, first + ci * C);
+    const __amdgpu_buffer_rsrc_t v = run_rows(v0, a.sh, val_pitch, 2 * NS, a.sh.run(a.first + ci, a.all));
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) vv[nt][r] = row_load1(v, val_row[r] + 32 * nt);
   };
-  auto load_t = [&](int ci) {
-    const __amdgpu_buffer_rsrc_t r = record(rec + static_cast<int64_t>(ci) * rec_bytes, a.lay.bytes);
+  auto load_t = [&]() {
+    const __amdgpu_buffer_rsrc_t r = record(rec, a.lay.bytes);
 #pragma unroll
     for (int s = 0; s < 2; ++s)
       if (lower_has(w, s))
@@ -406,20 +409,20 @@ __global__ __launch_bounds__(SAVE ? 256 : 512, SAVE ? 1 : 2) void k_delta_walk(W
         for (int i = 0; i < 3; ++i)
           tf[s][i] = record_frag(r, static_cast<int>(a.lay.t) + lower_at(w, s) * 3 * kB, i, lane16);
   };
-  auto load_gates = [&](int ci) {
-    const __amdgpu_buffer_rsrc_t r = record(rec + static_cast<int64_t>(ci) * rec_bytes, a.lay.bytes);
-    eg = gates4(r, 0);
+  auto load_eg = [&]() { eg = gates4(record(rec, a.lay.bytes), 0); };
+  auto load_keep = [&]() {
+    const __amdgpu_buffer_rsrc_t r = record(rec, a.lay.bytes);
     keep = gates4(r, 1);
     last = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, 4 * (C - 1), 0, 0));
   };
-  auto load_kt = [&](int ci) {
-    const __amdgpu_buffer_rsrc_t r = record(key + static_cast<int64_t>(ci) * key_bytes, a.lay.key_bytes);
+  auto load_kt = [&]() {
+    const __amdgpu_buffer_rsrc_t r = record(key, a.lay.key_bytes);
 #pragma unroll
     for (int st = 0; st < ST; ++st)
 #pragma unroll
       for (int s = 0; s < 2; ++s) ktf[st][s] = record_frag(r, ST * w * 2 * kB, 2 * st + s, lane16);
   };
-  load_rows(0), load_v(0), load_t(0), load_gates(0), load_kt(0);
+  load_rows(0), load_eg(), load_v(0), load_t(), load_keep(), load_kt();
 
   for (int ci = 0; ci < chunks; ++ci) {
     const int next = ci + 1 < chunks ? ci + 1 : ci;
@@ -464,7 +467,8 @@ __global__ __launch_bounds__(SAVE ? 256 : 512, SAVE ? 1 : 2) void k_delta_walk(W
 #pragma unroll
       for (int i = 0; i < 3; ++i) write4<C>(sR[i], 16 * nt + l16, 16 * w + 4 * q4, x[i]);
     }
-    load_v(next);
+    if (next > ci) rec += rec_bytes, key += key_bytes;
+    load_eg(), load_v(next);
     lds_barrier();
     f32x4 U[NT];
 #pragma unroll
@@ -480,7 +484,7 @@ __global__ __launch_bounds__(SAVE ? 256 : 512, SAVE ? 1 : 2) void k_delta_walk(W
         }
       U[nt] = sum3(u);
     }
-    load_t(next);
+    load_t();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       u32x2 p[3];
@@ -499,7 +503,7 @@ __global__ __launch_bounds__(SAVE ? 256 : 512, SAVE ? 1 : 2) void k_delta_walk(W
       }
     }
     const float decay = last;
-    load_gates(next);
+    load_keep();
     lds_barrier();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -517,7 +521,7 @@ __global__ __launch_bounds__(SAVE ? 256 : 512, SAVE ? 1 : 2) void k_delta_walk(W
 #pragma unroll
       for (int st = 0; st < ST; ++st) S[st][nt] = S[st][nt] * decay + sum3(add[st]);
     }
-    load_kt(next);
+    load_kt();
   }
   if (a.state_out) {
 #pragma unroll
@@ -547,6 +551,8 @@ struct StepArgs {
   float scale;
 };
 
+__device__ __forceinline__ int64_t step_token(const Shape& sh, int64_t p) { return sh.rev ? sh.L - 1 - p : p; }
+
 // Sum over the lanes that hold the same columns (lane % 8), in each of them.
 __device__ __forceinline__ float row_parts_sum(float v) {
   v += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x128, 0xf, 0xf, true));  // row_ror:8
@@ -575,7 +581,7 @@ __global__ __launch_bounds__(256) void k_delta_step(StepArgs a) {
   u32x2 vn;
   uint16_t dtn, bn;
   auto fetch = [&](int64_t p) {
-    const int64_t t = b * L + a.sh.token(p);
+    const int64_t t = b * L + step_token(a.sh, p);
 #pragma unroll
     for (int i = 0; i < R / 8; ++i) {
       kn[i] = *reinterpret_cast<const bf16x8*>(a.k + (t * a.sh.hk + kh) * DK + part * R + 8 * i);
@@ -609,7 +615,7 @@ __global__ __launch_bounds__(256) void k_delta_step(StepArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = row_parts_sum(o[e]) * a.scale;
     if (part == 0)
-      *reinterpret_cast<u32x2*>(a.out + ((b * L + a.sh.token(p)) * a.sh.heads + h) * a.dv + n) =
+      *reinterpret_cast<u32x2*>(a.out + ((b * L + step_token(a.sh, p)) * a.sh.heads + h) * a.dv + n) =
           __builtin_bit_cast(u32x2, __builtin_convertvector(o, bf16x4));
   }
   if (a.state_out) {
@@ -648,7 +654,7 @@ hipError_t launch_delta_prep(const DeltaArgs& in, const Plan& p, int64_t chunk0,
   const PrepArgs a{static_cast<const uint16_t*>(in.q), static_cast<const uint16_t*>(in.k),
                    static_cast<const uint16_t*>(in.dt), static_cast<const uint16_t*>(in.b), in.A, in.dt_bias,
                    w + p.head_off, w + p.key_off, Shape{in.seqlen, in.hk, in.heads, in.rev}, lay, chunk0, p.seg,
-                   in.scale};
+                   static_cast<int>(p.nchunk), in.scale};
   const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(in.heads), static_cast<unsigned>(in.batch));
   if (in.dk == 64) {
     if (grad) hipLaunchKernelGGL((k_delta_prep<64, true>), grid, dim3(256), 0, stream, a);
@@ -666,8 +672,8 @@ hipError_t launch_delta_walk(const DeltaArgs& in, const Plan& p, int64_t chunk0,
   const WalkArgs a{static_cast<const uint16_t*>(in.q), static_cast<const uint16_t*>(in.k),
                    static_cast<const uint16_t*>(in.v), static_cast<uint16_t*>(in.out), w + p.head_off, w + p.key_off,
                    state_in, state_out, reinterpret_cast<float*>(w + p.s_off), reinterpret_cast<float*>(w + p.u_off),
-                   Shape{in.seqlen, in.hk, in.heads, in.rev}, make_layout(in.dk, save), in.batch, in.dv, chunk0, chunks,
-                   p.seg, in.scale};
+                   Shape{in.seqlen, in.hk, in.heads, in.rev}, make_layout(in.dk, save), in.batch, in.dv, p.seg,
+                   static_cast<int>(chunk0), static_cast<int>(chunks), static_cast<int>(p.nchunk), in.scale};
   if (in.dk == 64) {
     if (save) launch_walk<64, true>(a, p.tiles, stream);
     else launch_walk<64, false>(a, p.tiles, stream);
