@@ -1,8 +1,13 @@
 // Product of 8-bit rows and 8-bit weights (OCP e4m3) with a scale for each row and 128 inputs, and for each 128 x 128
 // weights, for gfx950:
 //   out[m,n] = sum_j xs[m,j] ws[n/128,j] sum_{k in block j} x[m,k] w[n,k]
-// The inner sums run on the matrix cores (v_mfma_f32_16x16x128_f8f6f4: a block of 128 inputs in one instruction, products
-// of e4m3 values are exact, sums in fp32); the two scales are applied to each block's sum in fp32.
+// The inner sums run on the matrix cores, the two scales are applied to each block's sum in fp32.
+//
+// bf16 results take a block of 128 inputs in one v_mfma_f32_16x16x128_f8f6f4.  Its adder drops low bits of small products
+// beside large ones: sums of N(0, 1) operands come out 1.4e-5 off normwise (1.3e-5 of the terms' magnitudes at most on
+// single ones), the same as with the older 8-bit instructions; next to the result's own rounding, 2^-9, that does not
+// show.  fp32 results are to be better than that: there the operands are widened to bf16, which holds every e4m3 value,
+// and take four v_mfma_f32_16x16x32_bf16, whose sums are fp32 ones (1e-7), at half the rate.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -16,6 +21,11 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int BK = 128;  // inputs that share a scale
 
 struct Args {
   const uint8_t* x;
@@ -26,99 +36,237 @@ struct Args {
   int64_t m, n, k;
 };
 
-// Lane l holds row l % 16 of an operand at 16-byte chunks l / 16 and 4 + l / 16 of the block's 128 bytes (both operands
-// alike, so the order of the inputs within the block does not matter), and of the result column l % 16 (of the second
-// operand's rows), rows 4 (l / 16) .. + 3 (of the first's).
-__device__ __forceinline__ f32x4 mfma128(i32x8 a, i32x8 b) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0x7f7f7f7f, 0,
+// A row's 128 inputs as an operand: lane l holds row l % 16 at 16-byte chunks l / 16 and 4 + l / 16 (both operands alike,
+// so the order of the inputs within the block does not matter), and of the result column l % 16 (of the second operand's
+// rows), rows 4 (l / 16) .. + 3 (of the first's).
+template <bool WIDE>
+struct Operand;
+
+template <>
+struct Operand<false> {
+  i32x8 v;
+  __device__ __forceinline__ void set(i32x4 a, i32x4 b) { v = i32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}; }
+};
+
+template <>
+struct Operand<true> {
+  bf16x8 v[4];
+  static __device__ __forceinline__ bf16x8 widen(int a, int b) {
+    const bf16x2 p = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false);
+    const bf16x2 q = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true);
+    const bf16x2 r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false);
+    const bf16x2 s = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
+    return bf16x8{p[0], p[1], q[0], q[1], r[0], r[1], s[0], s[1]};
+  }
+  __device__ __forceinline__ void set(i32x4 a, i32x4 b) {
+    v[0] = widen(a[0], a[1]), v[1] = widen(a[2], a[3]), v[2] = widen(b[0], b[1]), v[3] = widen(b[2], b[3]);
+  }
+};
+
+__device__ __forceinline__ f32x4 block_sum(const Operand<false>& a, const Operand<false>& b) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0x7f7f7f7f, 0,
                                                           0x7f7f7f7f);
 }
 
-constexpr int BM = 128, BN = 128, BK = 128;
-
-__device__ __forceinline__ int chunk_at(int row, int c) { return row * BK + ((c ^ (row & 7)) << 4); }
-
-__device__ __forceinline__ i32x8 operand(const uint8_t* s, int row, int q4) {
-  const i32x4 a = *reinterpret_cast<const i32x4*>(s + chunk_at(row, q4));
-  const i32x4 b = *reinterpret_cast<const i32x4*>(s + chunk_at(row, 4 + q4));
-  return i32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+__device__ __forceinline__ f32x4 block_sum(const Operand<true>& a, const Operand<true>& b) {
+  f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], c, 0, 0, 0);
+  return c;
 }
 
 template <typename T>
 __device__ __forceinline__ void store4(f32x4 v, T* p) {
-  if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<f32x4*>(p) = v;
-  } else {
-    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-    *reinterpret_cast<bf16x4*>(p) = __builtin_convertvector(v, bf16x4);
-  }
+  if constexpr (sizeof(T) == 4) *reinterpret_cast<f32x4*>(p) = v;
+  else *reinterpret_cast<bf16x4*>(p) = __builtin_convertvector(v, bf16x4);
 }
 
-// 128 rows x 128 outputs per workgroup, 64 x 64 per wavefront.
-template <typename T>
-__global__ __launch_bounds__(256) void k_proj(Args a) {
+// Rows of 128 bytes in LDS, their 16-byte chunks permuted so that 16 lanes reading one chunk of 16 rows meet all banks.
+__device__ __forceinline__ int chunk_at(int row, int c) { return row * BK + ((c ^ (row & 7)) << 4); }
+
+template <bool WIDE>
+__device__ __forceinline__ void read_operand(const uint8_t* s, int row, int q4, Operand<WIDE>* o) {
+  o->set(*reinterpret_cast<const i32x4*>(s + chunk_at(row, q4)), *reinterpret_cast<const i32x4*>(s + chunk_at(row, 4 + q4)));
+}
+
+// A tile's rows of k bytes.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rows(const uint8_t* p, int64_t row0, int64_t rows, int64_t k,
+                                                            int tile) {
+  const int64_t n = min(rows - row0, static_cast<int64_t>(tile));
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p + row0 * k), static_cast<short>(0),
+                                           static_cast<int>(n * k), 0x00020000);
+}
+
+// 16 bytes a lane straight into LDS: lane l's go to `to` + 16 l.
+__device__ __forceinline__ void bring16(__amdgpu_buffer_rsrc_t r, uint8_t* to, uint32_t offset, int step) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, offset, step, 0, 0);
+}
+
+// Tiles of WM x WN wavefronts of 16 MI rows x 16 NI outputs (16 NI divides 128, so a wavefront's outputs share their
+// scales).  Each step of 128 inputs is brought into one of two LDS buffers by direct loads while the other is used, with
+// one barrier per step.
+template <typename T, bool WIDE, int MI, int NI, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void k_proj(Args a, int tiles_m, int tiles_n) {
+  constexpr int W = WM * WN, BM = 16 * MI * WM, BN = 16 * NI * WN;
   __shared__ __align__(16) uint8_t sx[2][BM * BK], sw[2][BN * BK];
-  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q4 = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * BM, n0 = static_cast<int64_t>(blockIdx.y) * BN;
-  const int64_t kb = a.k / BK;
-  const int wm = (w & 1) * 64, wn = (w >> 1) * 64;
-  i32x4 rx[4], rw[4];
-  auto fetch = [&](int64_t j) {
+  const int lane = threadIdx.x & 63, l16 = lane & 15, q4 = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // workgroups go to the eight XCDs in turn: each XCD takes a run of tiles of its own, in columns of 8 tiles of rows, so
+  // that rows and weights are reused in its L2
+  const int total = tiles_m * tiles_n, run = (total + 7) / 8;
+  const int id = static_cast<int>(blockIdx.x & 7) * run + static_cast<int>(blockIdx.x >> 3);
+  if (static_cast<int>(blockIdx.x >> 3) >= run || id >= total) return;
+  const int group = id / (8 * tiles_n), rows_here = min(8, tiles_m - 8 * group), in_group = id - group * 8 * tiles_n;
+  const int64_t m0 = static_cast<int64_t>(8 * group + in_group % rows_here) * BM;
+  const int64_t n0 = static_cast<int64_t>(in_group / rows_here) * BN;
+  const int wm = wave % WM * 16 * MI, wn = wave / WM * 16 * NI;
+  const int kb = static_cast<int>(a.k / BK);
+
+  // a wavefront brings 8 rows at a time; the lane's chunk within them is the one that belongs at the lane's place
+  const int lrow = lane >> 3, lchunk = ((lane & 7) ^ lrow) * 16;
+  const __amdgpu_buffer_rsrc_t rx = tile_rows(a.x, m0, a.m, a.k, BM), rw = tile_rows(a.w, n0, a.n, a.k, BN);
+  constexpr int LX = BM / 8 / W, LW = BN / 8 / W;
+  uint32_t ox[LX], ow[LW];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = tid + 256 * i, row = c >> 3;
-      const int64_t m = m0 + row < a.m ? m0 + row : a.m - 1, n = n0 + row < a.n ? n0 + row : a.n - 1;
-      rx[i] = *reinterpret_cast<const i32x4*>(a.x + m * a.k + j * BK + (c & 7) * 16);
-      rw[i] = *reinterpret_cast<const i32x4*>(a.w + n * a.k + j * BK + (c & 7) * 16);
-    }
+  for (int i = 0; i < LX; ++i) {
+    const int64_t row = min(static_cast<int64_t>(8 * (i * W + wave) + lrow), a.m - m0 - 1);
+    ox[i] = static_cast<uint32_t>(row * a.k + lchunk);
+  }
+#pragma unroll
+  for (int i = 0; i < LW; ++i) {
+    const int64_t row = min(static_cast<int64_t>(8 * (i * W + wave) + lrow), a.n - n0 - 1);
+    ow[i] = static_cast<uint32_t>(row * a.k + lchunk);
+  }
+  auto bring = [&](int j) {
+#pragma unroll
+    for (int i = 0; i < LX; ++i) bring16(rx, sx[j & 1] + (i * W + wave) * 8 * BK, ox[i], j * BK);
+#pragma unroll
+    for (int i = 0; i < LW; ++i) bring16(rw, sw[j & 1] + (i * W + wave) * 8 * BK, ow[i], j * BK);
   };
-  f32x4 acc[4][4];
+  const float* xs[MI];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const float* xs[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < MI; ++i) {
     const int64_t m = m0 + wm + 16 * i + l16;
     xs[i] = a.xs + (m < a.m ? m : a.m - 1) * kb;
   }
-  const float* ws = a.ws + blockIdx.y * kb;
-  fetch(0);
-  for (int64_t j = 0; j < kb; ++j) {
-    uint8_t* bx = sx[j & 1];
-    uint8_t* bw = sw[j & 1];
+  const float* ws = a.ws + min((n0 + wn) / BK, (a.n - 1) / BK) * kb;
+
+  f32x4 acc[MI][NI];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = tid + 256 * i;
-      *reinterpret_cast<i32x4*>(bx + chunk_at(c >> 3, c & 7)) = rx[i];
-      *reinterpret_cast<i32x4*>(bw + chunk_at(c >> 3, c & 7)) = rw[i];
-    }
-    __syncthreads();
-    if (j + 1 < kb) fetch(j + 1);
-    i32x8 wf[4];
+  for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) wf[i] = operand(bw, wn + 16 * i + l16, q4);
-    const float s = ws[j];
+    for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float sc[MI];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const i32x8 xf = operand(bx, wm + 16 * i + l16, q4);
-      const float c = xs[i][j] * s;
+  for (int i = 0; i < MI; ++i) sc[i] = xs[i][0];
+  bring(0);
+  for (int j = 0; j < kb; ++j) {
+    __syncthreads();  // waits for this wavefront's loads too
+    const int next = j + 1 < kb ? j + 1 : j;
+    float s[MI];
+    const float wsj = ws[j];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) acc[i][n] += mfma128(wf[n], xf) * c;
+    for (int i = 0; i < MI; ++i) s[i] = sc[i] * wsj;
+    if (j + 1 < kb) bring(j + 1);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) sc[i] = xs[i][next];
+    Operand<WIDE> wf[NI];
+#pragma unroll
+    for (int n = 0; n < NI; ++n) read_operand(sw[j & 1], wn + 16 * n + l16, q4, &wf[n]);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      Operand<WIDE> xf;
+      read_operand(sx[j & 1], wm + 16 * i + l16, q4, &xf);
+#pragma unroll
+      for (int n = 0; n < NI; ++n) acc[i][n] += block_sum(wf[n], xf) * s[i];
     }
   }
   T* out = static_cast<T*>(a.out);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < MI; ++i) {
     const int64_t m = m0 + wm + 16 * i + l16;
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
+    for (int n = 0; n < NI; ++n) {
       const int64_t col = n0 + wn + 16 * n + 4 * q4;
       if (m < a.m && col < a.n) store4<T>(acc[i][n], out + m * a.n + col);
     }
   }
+}
+
+// Few rows: the weights pass through once and bound the call.  A workgroup takes 16 outputs of all rows (16 MI of them); its
+// eight wavefronts take every eighth block of inputs, straight into registers, and add their sums in LDS.
+template <typename T, bool WIDE, int MI>
+__global__ __launch_bounds__(512) void k_proj_rows(Args a) {
+  constexpr int W = 8;
+  __shared__ float sums[W][MI][256];
+  const int lane = threadIdx.x & 63, l16 = lane & 15, q4 = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int kb = static_cast<int>(a.k / BK);
+  const uint8_t* wrow = a.w + min(n0 + l16, a.n - 1) * a.k + q4 * 16;
+  const float* ws = a.ws + n0 / BK * kb;
+  const uint8_t* xrow[MI];
+  const float* xs[MI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int64_t m = min(static_cast<int64_t>(16 * i + l16), a.m - 1);
+    xrow[i] = a.x + m * a.k + q4 * 16;
+    xs[i] = a.xs + m * kb;
+  }
+  f32x4 acc[MI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+  for (int j = wave; j < kb; j += W) {
+    Operand<WIDE> wf;
+    wf.set(__builtin_nontemporal_load(reinterpret_cast<const i32x4*>(wrow + static_cast<int64_t>(j) * BK)),
+           __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(wrow + static_cast<int64_t>(j) * BK + 64)));
+    const float wsj = ws[j];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      Operand<WIDE> xf;
+      xf.set(*reinterpret_cast<const i32x4*>(xrow[i] + static_cast<int64_t>(j) * BK),
+             *reinterpret_cast<const i32x4*>(xrow[i] + static_cast<int64_t>(j) * BK + 64));
+      acc[i] += block_sum(wf, xf) * (xs[i][j] * wsj);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MI; ++i) *reinterpret_cast<f32x4*>(&sums[wave][i][4 * lane]) = acc[i];
+  __syncthreads();
+  T* out = static_cast<T*>(a.out);
+  for (int i = wave; i < MI; i += W) {
+    f32x4 t = *reinterpret_cast<const f32x4*>(&sums[0][i][4 * lane]);
+#pragma unroll
+    for (int v = 1; v < W; ++v) t += *reinterpret_cast<const f32x4*>(&sums[v][i][4 * lane]);
+    const int64_t m = 16 * i + l16, col = n0 + 4 * q4;
+    if (m < a.m && col < a.n) store4<T>(t, out + m * a.n + col);
+  }
+}
+
+template <typename T, bool WIDE, int MI, int NI, int WM, int WN>
+void launch_tiles(const Args& a, hipStream_t stream) {
+  constexpr int BM = 16 * MI * WM, BN = 16 * NI * WN;
+  const int64_t tm = (a.m + BM - 1) / BM, tn = (a.n + BN - 1) / BN;
+  const dim3 grid(static_cast<unsigned>((tm * tn + 7) / 8 * 8));
+  hipLaunchKernelGGL((k_proj<T, WIDE, MI, NI, WM, WN>), grid, dim3(64 * WM * WN), 0, stream, a, static_cast<int>(tm),
+                     static_cast<int>(tn));
+}
+
+template <typename T, bool WIDE>
+void launch_typed(const Args& a, hipStream_t stream) {
+  if (a.m <= 64) {
+    const dim3 grid(static_cast<unsigned>((a.n + 15) / 16));
+    if (a.m <= 16) hipLaunchKernelGGL((k_proj_rows<T, WIDE, 1>), grid, dim3(512), 0, stream, a);
+    else if (a.m <= 32) hipLaunchKernelGGL((k_proj_rows<T, WIDE, 2>), grid, dim3(512), 0, stream, a);
+    else hipLaunchKernelGGL((k_proj_rows<T, WIDE, 4>), grid, dim3(512), 0, stream, a);
+    return;
+  }
+  const int64_t t128 = (a.m + 127) / 128 * ((a.n + 127) / 128), t256 = (a.m + 255) / 256 * ((a.n + 255) / 256);
+  if constexpr (!WIDE) {
+    if (t256 >= 512) return launch_tiles<T, WIDE, 8, 4, 2, 4>(a, stream);
+  }
+  if (t128 >= 512) launch_tiles<T, WIDE, 4, 4, 2, 2>(a, stream);
+  else launch_tiles<T, WIDE, 2, 2, 2, 2>(a, stream);
 }
 
 }  // namespace
@@ -126,9 +274,8 @@ __global__ __launch_bounds__(256) void k_proj(Args a) {
 hipError_t launch_proj(const ProjArgs& in, hipStream_t stream) {
   const Args a{static_cast<const uint8_t*>(in.x), in.xs, static_cast<const uint8_t*>(in.w), in.ws, in.out, in.m, in.n,
                in.k};
-  const dim3 grid(static_cast<unsigned>((in.m + BM - 1) / BM), static_cast<unsigned>((in.n + BN - 1) / BN));
-  if (in.out_dtype == 1) hipLaunchKernelGGL((k_proj<bf16_t>), grid, dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((k_proj<float>), grid, dim3(256), 0, stream, a);
+  if (in.out_dtype == 1) launch_typed<bf16_t, false>(a, stream);
+  else launch_typed<float, true>(a, stream);
   return hipGetLastError();
 }
 
