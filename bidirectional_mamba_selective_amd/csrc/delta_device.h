@@ -7,6 +7,7 @@
 
 #include "delta_plan.h"
 #include "device_math.h"
+#include "lds_barrier.h"
 
 namespace bimamba {
 namespace delta {
@@ -123,14 +124,6 @@ struct Own<2> {
 template <int ST>
 __device__ __forceinline__ int state_row(int w, int t, int m) {
   return 16 * ST * w + 4 * ST * (m >> 2) + 4 * t + (m & 3);
-}
-
-// A barrier for what passes through LDS only: __syncthreads would also wait for every global load and store in flight, and
-// with it for the next chunk's operands.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // Where the operands of a triangular 64 x 64 matrix lie in a record.  lower: rows 16 w, k 32 s, entries with k <= row;

@@ -13,6 +13,7 @@
 
 #include "device_math.h"
 #include "launch.h"
+#include "lds_barrier.h"
 
 namespace bimamba {
 namespace proj {
@@ -84,9 +85,10 @@ __device__ __forceinline__ void store4(f32x4 v, T* p) {
 // Rows of 128 bytes in LDS, their 16-byte chunks permuted so that 16 lanes reading one chunk of 16 rows meet all banks.
 __device__ __forceinline__ int chunk_at(int row, int c) { return row * BK + ((c ^ (row & 7)) << 4); }
 
+// The operand of rows row + 16 i: lo and hi point at the two chunks of row (the permutation has a period of 8 rows).
 template <bool WIDE>
-__device__ __forceinline__ void read_operand(const uint8_t* s, int row, int q4, Operand<WIDE>* o) {
-  o->set(*reinterpret_cast<const i32x4*>(s + chunk_at(row, q4)), *reinterpret_cast<const i32x4*>(s + chunk_at(row, 4 + q4)));
+__device__ __forceinline__ void read_operand(const uint8_t* lo, const uint8_t* hi, int i, Operand<WIDE>* o) {
+  o->set(*reinterpret_cast<const i32x4*>(lo + 16 * BK * i), *reinterpret_cast<const i32x4*>(hi + 16 * BK * i));
 }
 
 // A tile's rows of k bytes.
@@ -97,18 +99,15 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rows(const uint8_t* p, in
                                            static_cast<int>(n * k), 0x00020000);
 }
 
-// 16 bytes a lane straight into LDS: lane l's go to `to` + 16 l.
-__device__ __forceinline__ void bring16(__amdgpu_buffer_rsrc_t r, uint8_t* to, uint32_t offset, int step) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, offset, step, 0, 0);
-}
-
 // Tiles of WM x WN wavefronts of 16 MI rows x 16 NI outputs (16 NI divides 128, so a wavefront's outputs share their
-// scales).  Each step of 128 inputs is brought into one of two LDS buffers by direct loads while the other is used, with
-// one barrier per step.
+// scales).  Two LDS buffers and one barrier per step of 128 inputs: the next step's rows are loaded into registers while
+// the products of this one run and are written to the other buffer after them.
 template <typename T, bool WIDE, int MI, int NI, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_proj(Args a, int tiles_m, int tiles_n) {
-  constexpr int W = WM * WN, BM = 16 * MI * WM, BN = 16 * NI * WN;
+  constexpr int W = WM * WN, BM = 16 * MI * WM, BN = 16 * NI * WN, LX = BM / 8 / W, LW = BN / 8 / W;
   __shared__ __align__(16) uint8_t sx[2][BM * BK], sw[2][BN * BK];
+  __shared__ float ss[2][64 * W];  // the rows' scales of the step (each thread brings one; those past BM are not used)
+  static_assert(64 * W >= BM, "a thread per row");
   const int lane = threadIdx.x & 63, l16 = lane & 15, q4 = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // workgroups go to the eight XCDs in turn: each XCD takes a run of tiles of its own, in columns of 8 tiles of rows, so
@@ -122,64 +121,73 @@ __global__ __launch_bounds__(64 * WM * WN) void k_proj(Args a, int tiles_m, int 
   const int wm = wave % WM * 16 * MI, wn = wave / WM * 16 * NI;
   const int kb = static_cast<int>(a.k / BK);
 
-  // a wavefront brings 8 rows at a time; the lane's chunk within them is the one that belongs at the lane's place
-  const int lrow = lane >> 3, lchunk = ((lane & 7) ^ lrow) * 16;
+  // thread t brings chunk t % 8 of rows t / 8 + 8 W i; rows past the end come from the last one and are not stored
+  const int brow = threadIdx.x >> 3, bat = chunk_at(brow, threadIdx.x & 7);
   const __amdgpu_buffer_rsrc_t rx = tile_rows(a.x, m0, a.m, a.k, BM), rw = tile_rows(a.w, n0, a.n, a.k, BN);
-  constexpr int LX = BM / 8 / W, LW = BN / 8 / W;
   uint32_t ox[LX], ow[LW];
 #pragma unroll
-  for (int i = 0; i < LX; ++i) {
-    const int64_t row = min(static_cast<int64_t>(8 * (i * W + wave) + lrow), a.m - m0 - 1);
-    ox[i] = static_cast<uint32_t>(row * a.k + lchunk);
-  }
+  for (int i = 0; i < LX; ++i)
+    ox[i] = static_cast<uint32_t>(min(static_cast<int64_t>(brow + 8 * W * i), a.m - m0 - 1) * a.k) + (threadIdx.x & 7) * 16;
 #pragma unroll
-  for (int i = 0; i < LW; ++i) {
-    const int64_t row = min(static_cast<int64_t>(8 * (i * W + wave) + lrow), a.n - n0 - 1);
-    ow[i] = static_cast<uint32_t>(row * a.k + lchunk);
-  }
-  auto bring = [&](int j) {
-#pragma unroll
-    for (int i = 0; i < LX; ++i) bring16(rx, sx[j & 1] + (i * W + wave) * 8 * BK, ox[i], j * BK);
-#pragma unroll
-    for (int i = 0; i < LW; ++i) bring16(rw, sw[j & 1] + (i * W + wave) * 8 * BK, ow[i], j * BK);
-  };
-  const float* xs[MI];
-#pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int64_t m = m0 + wm + 16 * i + l16;
-    xs[i] = a.xs + (m < a.m ? m : a.m - 1) * kb;
-  }
+  for (int i = 0; i < LW; ++i)
+    ow[i] = static_cast<uint32_t>(min(static_cast<int64_t>(brow + 8 * W * i), a.n - n0 - 1) * a.k) + (threadIdx.x & 7) * 16;
+  const float* xs = a.xs + min(m0 + threadIdx.x, a.m - 1) * kb;
   const float* ws = a.ws + min((n0 + wn) / BK, (a.n - 1) / BK) * kb;
+
+  i32x4 gx[LX], gw[LW];
+  float gs = 0.0f, ws_next;
+  auto fetch = [&](int j) {
+    gs = xs[j];
+    ws_next = ws[j];
+#pragma unroll
+    for (int i = 0; i < LX; ++i)
+      gx[i] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, ox[i], j * BK, 0));
+#pragma unroll
+    for (int i = 0; i < LW; ++i)
+      gw[i] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, ow[i], j * BK, 0));
+  };
+  auto put = [&](int j) {
+    ss[j & 1][threadIdx.x] = gs;
+#pragma unroll
+    for (int i = 0; i < LX; ++i) *reinterpret_cast<i32x4*>(sx[j & 1] + 8 * W * BK * i + bat) = gx[i];
+#pragma unroll
+    for (int i = 0; i < LW; ++i) *reinterpret_cast<i32x4*>(sw[j & 1] + 8 * W * BK * i + bat) = gw[i];
+  };
 
   f32x4 acc[MI][NI];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float sc[MI];
-#pragma unroll
-  for (int i = 0; i < MI; ++i) sc[i] = xs[i][0];
-  bring(0);
+  const int xlo = chunk_at(wm + l16, q4), xhi = chunk_at(wm + l16, 4 + q4);
+  const int wlo = chunk_at(wn + l16, q4), whi = chunk_at(wn + l16, 4 + q4);
+  fetch(0);
+  put(0);
   for (int j = 0; j < kb; ++j) {
-    __syncthreads();  // waits for this wavefront's loads too
-    const int next = j + 1 < kb ? j + 1 : j;
-    float s[MI];
-    const float wsj = ws[j];
+    const float wsj = ws_next;
+    fetch(j + 1 < kb ? j + 1 : j);  // no branch in the loop: the compiler would move the products across it
+    lds_barrier();
+    const uint8_t *cx = sx[j & 1], *cw = sw[j & 1];
+    Operand<WIDE> wf[NI], xf[2];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) s[i] = sc[i] * wsj;
-    if (j + 1 < kb) bring(j + 1);
+    for (int n = 0; n < NI; ++n) read_operand(cw + wlo, cw + whi, n, &wf[n]);
+    read_operand(cx + xlo, cx + xhi, 0, &xf[0]);
+    // a row tile's products are scaled, one by one, between those of the next
+    f32x4 t[NI];
+    float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < MI; ++i) sc[i] = xs[i][next];
-    Operand<WIDE> wf[NI];
+    for (int i = 0; i <= MI; ++i) {
+      const float next = i < MI ? ss[j & 1][wm + 16 * i + l16] * wsj : 0.0f;
+      if (i + 1 < MI) read_operand(cx + xlo, cx + xhi, i + 1, &xf[(i + 1) & 1]);
 #pragma unroll
-    for (int n = 0; n < NI; ++n) read_operand(sw[j & 1], wn + 16 * n + l16, q4, &wf[n]);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      Operand<WIDE> xf;
-      read_operand(sx[j & 1], wm + 16 * i + l16, q4, &xf);
-#pragma unroll
-      for (int n = 0; n < NI; ++n) acc[i][n] += block_sum(wf[n], xf) * s[i];
+      for (int n = 0; n < NI; ++n) {
+        if (i > 0) acc[i - 1][n] += t[n] * s;
+        if (i < MI) t[n] = block_sum(wf[n], xf[i & 1]);
+      }
+      s = next;
     }
+    // the other buffer was last read before this step's barrier
+    put(j + 1);
   }
   T* out = static_cast<T*>(a.out);
 #pragma unroll
