@@ -100,8 +100,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rows(const uint8_t* p, in
 }
 
 // Tiles of WM x WN wavefronts of 16 MI rows x 16 NI outputs (16 NI divides 128, so a wavefront's outputs share their
-// scales).  Two LDS buffers and one barrier per step of 128 inputs: the next step's rows are loaded into registers while
-// the products of this one run and are written to the other buffer after them.
+// scales).  Two LDS buffers and one barrier per step of 128 inputs: rows are loaded into registers two steps ahead and
+// written to the other buffer one step ahead, in pieces that are spread over the step's products (all at once, as a burst
+// of every wavefront, the loads took longer than a step: 626 us at 16384 x 8192 x 4096).
 template <typename T, bool WIDE, int MI, int NI, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_proj(Args a, int tiles_m, int tiles_n) {
   constexpr int W = WM * WN, BM = 16 * MI * WM, BN = 16 * NI * WN, LX = BM / 8 / W, LW = BN / 8 / W;
@@ -134,24 +135,17 @@ __global__ __launch_bounds__(64 * WM * WN) void k_proj(Args a, int tiles_m, int 
   const float* xs = a.xs + min(m0 + threadIdx.x, a.m - 1) * kb;
   const float* ws = a.ws + min((n0 + wn) / BK, (a.n - 1) / BK) * kb;
 
-  i32x4 gx[LX], gw[LW];
-  float gs = 0.0f, ws_next;
-  auto fetch = [&](int j) {
-    gs = xs[j];
-    ws_next = ws[j];
-#pragma unroll
-    for (int i = 0; i < LX; ++i)
-      gx[i] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, ox[i], j * BK, 0));
-#pragma unroll
-    for (int i = 0; i < LW; ++i)
-      gw[i] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, ow[i], j * BK, 0));
+  // a step's rows in pieces: LX of x, LW of w
+  constexpr int kPieces = LX + LW;
+  i32x4 g[kPieces];
+  float gs, gws;
+  auto fetch = [&](int p, int j) {
+    g[p] = __builtin_bit_cast(i32x4, p < LX ? __builtin_amdgcn_raw_buffer_load_b128(rx, ox[p < LX ? p : 0], j * BK, 0)
+                                            : __builtin_amdgcn_raw_buffer_load_b128(rw, ow[p < LX ? 0 : p - LX], j * BK, 0));
   };
-  auto put = [&](int j) {
-    ss[j & 1][threadIdx.x] = gs;
-#pragma unroll
-    for (int i = 0; i < LX; ++i) *reinterpret_cast<i32x4*>(sx[j & 1] + 8 * W * BK * i + bat) = gx[i];
-#pragma unroll
-    for (int i = 0; i < LW; ++i) *reinterpret_cast<i32x4*>(sw[j & 1] + 8 * W * BK * i + bat) = gw[i];
+  auto fetch_scales = [&](int j) { gs = xs[j], gws = ws[j]; };
+  auto put = [&](int p, int j) {
+    *reinterpret_cast<i32x4*>((p < LX ? sx[j & 1] + 8 * W * BK * p : sw[j & 1] + 8 * W * BK * (p - LX)) + bat) = g[p];
   };
 
   f32x4 acc[MI][NI];
@@ -161,18 +155,27 @@ __global__ __launch_bounds__(64 * WM * WN) void k_proj(Args a, int tiles_m, int 
     for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int xlo = chunk_at(wm + l16, q4), xhi = chunk_at(wm + l16, 4 + q4);
   const int wlo = chunk_at(wn + l16, q4), whi = chunk_at(wn + l16, 4 + q4);
-  fetch(0);
-  put(0);
+  fetch_scales(0);
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) fetch(p, 0);
+  float wsj = gws;
+  ss[0][threadIdx.x] = gs;
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) put(p, 0);
+  fetch_scales(min(1, kb - 1));
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) fetch(p, min(1, kb - 1));
   for (int j = 0; j < kb; ++j) {
-    const float wsj = ws_next;
-    fetch(j + 1 < kb ? j + 1 : j);  // no branch in the loop: the compiler would move the products across it
+    // no branch in the loop: the compiler would move the products across it
+    const int ahead = min(j + 2, kb - 1);
     lds_barrier();
     const uint8_t *cx = sx[j & 1], *cw = sw[j & 1];
     Operand<WIDE> wf[NI], xf[2];
 #pragma unroll
     for (int n = 0; n < NI; ++n) read_operand(cw + wlo, cw + whi, n, &wf[n]);
     read_operand(cx + xlo, cx + xhi, 0, &xf[0]);
-    // a row tile's products are scaled, one by one, between those of the next
+    // a row tile's products are scaled, one by one, between those of the next; the pieces that came in during the last
+    // step go into the other buffer, and those of the step after next are asked for, evenly over the step
     f32x4 t[NI];
     float s = 0.0f;
 #pragma unroll
@@ -185,9 +188,15 @@ __global__ __launch_bounds__(64 * WM * WN) void k_proj(Args a, int tiles_m, int 
         if (i < MI) t[n] = block_sum(wf[n], xf[i & 1]);
       }
       s = next;
+#pragma unroll
+      for (int p = kPieces * i / MI; p < kPieces * (i + 1) / MI && p < kPieces; ++p) {
+        put(p, j + 1);
+        fetch(p, ahead);
+      }
     }
-    // the other buffer was last read before this step's barrier
-    put(j + 1);
+    ss[(j + 1) & 1][threadIdx.x] = gs;
+    wsj = gws;
+    fetch_scales(ahead);
   }
   T* out = static_cast<T*>(a.out);
 #pragma unroll
