@@ -311,8 +311,14 @@ struct GradArgs {
   float scale;
 };
 
-__device__ __forceinline__ f32x8 load_f32x8(const float* p) {
-  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+// n fp32 values as a buffer, and 8 of them at byte offset + step.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t floats(const float* p, int n) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p), static_cast<short>(0), n * 4, 0x00020000);
+}
+
+__device__ __forceinline__ f32x8 load_f32x8(__amdgpu_buffer_rsrc_t r, int offset, int step) {
+  const f32x4 a = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, offset, step, 0));
+  const f32x4 b = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, offset + 16, step, 0));
   return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
@@ -337,31 +343,30 @@ __device__ __forceinline__ float sum_rows(float v) {
   return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
+// Eight wavefronts: wavefront w + 4 c takes the chunk's tokens 16 w .. + 15 and, of the tokens or columns that it meets
+// them with, the tiles of parity c.  What ends in an fp32 result (the sums of P, s and e) is formed from three parts of each
+// fp32 operand, D1 and D2 as operands of the bf16 results from two.
 template <int DK, int DV>
-__global__ __launch_bounds__(256) void k_delta_grads(GradArgs a) {
-  constexpr int KS = DK / 32, ST = DK / 64, VS = DV / 32, KT = DK / 16, kRow = DK + 8, kPitch = C + 1;
+__global__ __launch_bounds__(512, 2) void k_delta_grads(GradArgs a) {
+  constexpr int KS = DK / 32, ST = DK / 64, VS = DV / 32, KT = DK / 32, kRow = DK + 8, kPitch = C + 1;
   __shared__ __align__(16) uint16_t sD1[2][C * C], sD1t[2][C * C], sD2[2][C * C], sD2t[2][C * C];
   __shared__ __align__(16) uint16_t sQ[C * kRow], sK[C * kRow];
   __shared__ float sP[C * kPitch];
-  __shared__ float sHi[C], sLo[C], sEg[C], sKeep[C], sS0[C], sS1[C], sDb[C], sAcc[4][C], sDot[4];
+  __shared__ __align__(16) float sHi[C], sLo[C], sEg[C], sKeep[C];
+  __shared__ float sS0[2][C], sS1[2][C], sDb[C], sAcc[8][C], sDot[8];
   const int lane = threadIdx.x & 63, l16 = lane & 15, q4 = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave & 3, c = wave >> 2;
   const int64_t ci = blockIdx.x, kh = blockIdx.y, b = blockIdx.z, L = a.sh.L, share = a.sh.heads / a.sh.hk;
-  const int64_t t0 = static_cast<int64_t>(a.sh.run(static_cast<int>(ci), static_cast<int>(a.chunks))) * C;
+  const int run = a.sh.run(static_cast<int>(ci), static_cast<int>(a.chunks));
+  const int64_t t0 = static_cast<int64_t>(run) * C;
   const unsigned char* key = a.keys + ((b * a.sh.hk + kh) * a.chunks + ci) * a.lay.key_bytes;
 
-  bf16x8 kf[KS], qf[KS];
-  {
-    const int64_t t = t0 + a.sh.place(16 * w + l16);
-    const int64_t row = ((b * L + (t < L ? t : L - 1)) * a.sh.hk + kh) * DK + 8 * q4;
+  const int64_t my_t = t0 + a.sh.place(16 * w + l16), my_row = b * L + (my_t < L ? my_t : L - 1);
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      kf[s] = *reinterpret_cast<const bf16x8*>(a.k + row + 32 * s);
-      qf[s] = *reinterpret_cast<const bf16x8*>(a.q + row + 32 * s);
-      if (t >= L) kf[s] = qf[s] = zero8();
-      *reinterpret_cast<bf16x8*>(sK + (16 * w + l16) * kRow + 32 * s + 8 * q4) = kf[s];
-      *reinterpret_cast<bf16x8*>(sQ + (16 * w + l16) * kRow + 32 * s + 8 * q4) = qf[s];
-    }
+  for (int s = 0; s < KS; ++s) {
+    bf16x8 v = *reinterpret_cast<const bf16x8*>((c ? a.q : a.k) + (my_row * a.sh.hk + kh) * DK + 32 * s + 8 * q4);
+    if (my_t >= L) v = zero8();
+    *reinterpret_cast<bf16x8*>((c ? sQ : sK) + (16 * w + l16) * kRow + 32 * s + 8 * q4) = v;
   }
   f32x4 dq[KT], dk[KT];
 #pragma unroll
@@ -371,67 +376,100 @@ __global__ __launch_bounds__(256) void k_delta_grads(GradArgs a) {
     const int64_t h = kh * share + g, bh = b * a.sh.heads + h, hc = bh * a.chunks + ci;
     const float* gates = reinterpret_cast<const float*>(a.heads + hc * a.lay.bytes);
     lds_barrier();  // the previous head's readers of what is written here
-    if (w == 0) sEg[lane] = gates[lane], sKeep[lane] = gates[C + lane];
-    if (w == 1) sHi[lane] = gates[2 * C + lane], sLo[lane] = gates[3 * C + lane];
-    // this wavefront's rows of dO, dR and U as operands
-    bf16x8 od[VS], rd[VS][2], ud[VS][2];
-    {
-      const int64_t t = t0 + a.sh.place(16 * w + l16);
-      const uint16_t* row = a.dout + ((b * L + (t < L ? t : L - 1)) * a.sh.heads + h) * DV + 8 * q4;
-      float dot = 0.0f;
-      const float beta = gates[4 * C + 16 * w + l16];
-      const float rb = beta > 1e-30f ? 1.0f / beta : 0.0f;
+    if (wave == 0) sEg[lane] = gates[lane], sKeep[lane] = gates[C + lane];
+    if (wave == 1) sHi[lane] = gates[2 * C + lane], sLo[lane] = gates[3 * C + lane];
+    const float beta = gates[4 * C + 16 * w + l16];
+    const float rb = beta > 1e-30f ? 1.0f / beta : 0.0f;
+    // 32 columns of the value head at a time (not unrolled: brought forward, the loads of several do not fit the registers)
+    f32x4 d1[2], d2[2], t1[KT], t2[KT], t3[KT];
+    float dot = 0.0f, ur = 0.0f;
 #pragma unroll
-      for (int s = 0; s < VS; ++s) {
-        od[s] = *reinterpret_cast<const bf16x8*>(row + 32 * s);
-        if (t >= L) od[s] = zero8();
-        const f32x8 r = load_f32x8(a.drs + (hc * C + 16 * w + l16) * DV + 32 * s + 8 * q4);
-        const f32x8 u = load_f32x8(a.us + (hc * C + 16 * w + l16) * DV + 32 * s + 8 * q4);
+    for (int i = 0; i < KT; ++i) t1[i] = t2[i] = t3[i] = zero4();
+    d1[0] = d1[1] = d2[0] = d2[1] = zero4();
+    const int val_pitch = static_cast<int>(a.sh.heads) * DV * 2;
+    const __amdgpu_buffer_rsrc_t go = run_rows(a.dout + (b * L * a.sh.heads + h) * DV, a.sh, val_pitch, DV * 2, run);
+    const __amdgpu_buffer_rsrc_t gr = floats(a.drs + hc * C * DV, C * DV), gu = floats(a.us + hc * C * DV, C * DV);
+    const __amdgpu_buffer_rsrc_t gs = floats(a.states + hc * DK * DV, DK * DV), gd = floats(a.dstates + hc * DK * DV, DK * DV);
+    const int orow = a.sh.place(16 * w + l16) * val_pitch + 16 * q4;
+    const int urow = (l16 * DV + 8 * q4) * 4;  // of 16 rows of U or dR
+    int srow[KT];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dot = fmaf(u[e] * rb, r[e], dot);
-        split8(r, rd[s]);
-        split8(u, ud[s]);
+    for (int i = 0; i < KT; ++i) srow[i] = (state_row<ST>((2 * i + c) / ST, (2 * i + c) % ST, l16) * DV + 8 * q4) * 4;
+#pragma unroll 1
+    for (int s = 0; s < VS; ++s) {
+      bf16x8 rd[3], ud[3];
+      const bf16x8 od[1] = {row_load8(go, orow + 64 * s)};
+      const f32x8 r = load_f32x8(gr, urow + 64 * DV * w, 128 * s), u = load_f32x8(gu, urow + 64 * DV * w, 128 * s);
+      f32x8 st[2], ds[2];
+      st[0] = load_f32x8(gs, srow[0], 128 * s);
+      ds[0] = load_f32x8(gd, srow[0], 128 * s);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ur = fmaf(u[e] * rb, r[e], ur);
+      split8(r, rd);
+      split8(u, ud);
+#pragma unroll
+      for (int i = 0; i < KT; ++i) {
+        const f32x8 x = st[i & 1], z = ds[i & 1];
+        if (i + 1 < KT) {
+          st[(i + 1) & 1] = load_f32x8(gs, srow[i + 1], 128 * s);
+          ds[(i + 1) & 1] = load_f32x8(gd, srow[i + 1], 128 * s);
+        }
+        if (((KT == 4 ? i : 2 * (s & 1) + i) & 3) == w) {  // every value of the states in one wavefront
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dot = fmaf(x[e], z[e], dot);
+        }
+        bf16x8 y[3];
+        split8(x, y);
+        t1[i] = mfma_parts(od, y, t1[i]);
+        t2[i] = mfma_parts(rd, y, t2[i]);
+        split8(z, y);
+        t3[i] = mfma_parts(ud, y, t3[i]);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      dot = sum_rows(dot);
-      if (q4 == 0) sDb[16 * w + l16] = dot;
+#pragma unroll
+      for (int jj = 0; jj < 2; ++jj)
+        if (2 * jj + c <= w) {
+          bf16x8 y[3];
+          split8(load_f32x8(gu, urow + 64 * DV * (2 * jj + c), 128 * s), y);
+          d1[jj] = mfma_parts(od, y, d1[jj]);
+          d2[jj] = mfma_parts(rd, y, d2[jj]);
+        }
     }
+    ur = sum_rows(ur);
+    if (c == 0 && q4 == 0) sDb[16 * w + l16] = ur;
     lds_barrier();
     const f32x4 eg = *reinterpret_cast<const f32x4*>(sEg + 16 * w + 4 * q4);
     const f32x4 keep = *reinterpret_cast<const f32x4*>(sKeep + 16 * w + 4 * q4);
 
-    for (int j = 0; j < 4; ++j) {
-      f32x4 d1 = zero4(), d2 = zero4(), pr = zero4();
+#pragma unroll
+    for (int jj = 0; jj < 2; ++jj) {
+      const int j = 2 * jj + c;
+      f32x4 pr = zero4();
       if (j <= w) {
         f32x4 qk = zero4(), kk = zero4();
 #pragma unroll
-        for (int s = 0; s < VS; ++s) {
-          bf16x8 u[2];
-          split8(load_f32x8(a.us + (hc * C + 16 * j + l16) * DV + 32 * s + 8 * q4), u);
-          const bf16x8 x[1] = {od[s]};
-          d1 = mfma_parts(x, u, d1);
-          d2 = mfma_parts(rd[s], u, d2);
-        }
-#pragma unroll
         for (int s = 0; s < KS; ++s) {
           const bf16x8 o = *reinterpret_cast<const bf16x8*>(sK + (16 * j + l16) * kRow + 32 * s + 8 * q4);
-          qk = mfma(qf[s], o, qk);
-          kk = mfma(kf[s], o, kk);
+          const bf16x8 kw = *reinterpret_cast<const bf16x8*>(sK + (16 * w + l16) * kRow + 32 * s + 8 * q4);
+          const bf16x8 qw = *reinterpret_cast<const bf16x8*>(sQ + (16 * w + l16) * kRow + 32 * s + 8 * q4);
+          qk = mfma(qw, o, qk);
+          kk = mfma(kw, o, kk);
         }
         const int col = 16 * j + l16;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int row = 16 * w + 4 * q4 + r;
           const float d = col <= row ? ex((sHi[row] - sHi[col]) + (sLo[row] - sLo[col])) : 0.0f;
-          d1[r] = col <= row ? d1[r] * d * a.scale : 0.0f;
-          d2[r] = col < row ? -d2[r] * d : 0.0f;
-          pr[r] = col < row ? fmaf(d1[r], qk[r], d2[r] * kk[r]) : 0.0f;
+          d1[jj][r] = col <= row ? d1[jj][r] * d * a.scale : 0.0f;
+          d2[jj][r] = col < row ? -d2[jj][r] * d : 0.0f;
+          pr[r] = col < row ? fmaf(d1[jj][r], qk[r], d2[jj][r] * kk[r]) : 0.0f;
         }
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) sP[(16 * w + 4 * q4 + r) * kPitch + 16 * j + l16] = pr[r];
       u32x2 p1[2], p2[2];
-      split4(d1, p1);
-      split4(d2, p2);
+      split4(d1[jj], p1);
+      split4(d2[jj], p2);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         write4<C>(sD1t[i], 16 * j + l16, 16 * w + 4 * q4, p1[i]);
@@ -443,52 +481,36 @@ __global__ __launch_bounds__(256) void k_delta_grads(GradArgs a) {
         }
       }
     }
-    // products with the states
     f32x4 s0 = zero4(), s1 = zero4();
-    float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < KT; ++i) {
-      f32x4 t1 = zero4(), t2 = zero4(), t3 = zero4();
-#pragma unroll
-      for (int s = 0; s < VS; ++s) {
-        const int64_t at_row = (hc * DK + state_row<ST>(i / ST, i % ST, l16)) * DV + 32 * s + 8 * q4;
-        const f32x8 st = load_f32x8(a.states + at_row), ds = load_f32x8(a.dstates + at_row);
-        if ((i & 3) == w) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dot = fmaf(st[e], ds[e], dot);
-        }
-        bf16x8 y[2], z[2];
-        split8(st, y);
-        split8(ds, z);
-        const bf16x8 x[1] = {od[s]};
-        t1 = mfma_parts(x, y, t1);
-        t2 = mfma_parts(rd[s], y, t2);
-        t3 = mfma_parts(ud[s], z, t3);
-      }
-      t1 *= eg * a.scale;
-      t2 *= -eg;
-      t3 *= keep;
-      dq[i] += t1;
-      dk[i] += t2 + t3;
+      const int tile = 2 * i + c;
+      t1[i] *= eg * a.scale;
+      t2[i] *= -eg;
+      t3[i] *= keep;
+      dq[i] += t1[i];
+      dk[i] += t2[i] + t3[i];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int e = (16 * w + 4 * q4 + r) * kRow + state_row<ST>(i / ST, i % ST, l16);
+        const int e = (16 * w + 4 * q4 + r) * kRow + state_row<ST>(tile / ST, tile % ST, l16);
         const float kv = bf(sK[e]);
-        s0[r] = fmaf(bf(sQ[e]), t1[r], fmaf(kv, t2[r], s0[r]));
-        s1[r] = fmaf(kv, t3[r], s1[r]);
+        s0[r] = fmaf(bf(sQ[e]), t1[i][r], fmaf(kv, t2[i][r], s0[r]));
+        s1[r] = fmaf(kv, t3[i][r], s1[r]);
       }
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const float v0 = sum16(s0[r]), v1 = sum16(s1[r]);
-      if (l16 == 0) sS0[16 * w + 4 * q4 + r] = v0, sS1[16 * w + 4 * q4 + r] = v1;
+      if (l16 == 0) sS0[c][16 * w + 4 * q4 + r] = v0, sS1[c][16 * w + 4 * q4 + r] = v1;
     }
     dot = sum_rows(sum16(dot));
-    if (lane == 0) sDot[w] = dot;
+    if (lane == 0) sDot[wave] = dot;
     lds_barrier();
 
     // products within the chunk
-#pragma unroll
+    constexpr int kB = static_cast<int>(kFragBytes);
+    const __amdgpu_buffer_rsrc_t keys = record(key, a.lay.key_bytes);
+#pragma unroll 1
     for (int s = 0; s < 2; ++s) {
       bf16x8 d1[2], d2[2], d1t[2], d2t[2];
 #pragma unroll
@@ -500,24 +522,24 @@ __global__ __launch_bounds__(256) void k_delta_grads(GradArgs a) {
       }
 #pragma unroll
       for (int i = 0; i < KT; ++i) {
-        const bf16x8 kt[1] = {load_frag(key, 2 * i + s, lane)};
+        const bf16x8 kt[1] = {record_frag(keys, 2 * c * kB, 4 * i + s, 16 * lane)};
         if (lower_has(w, s)) {
           dq[i] = mfma_parts(d1, kt, dq[i]);
           dk[i] = mfma_parts(d2, kt, dk[i]);
         }
         if (upper_has(w, s)) {
-          const bf16x8 qt[1] = {load_frag(key, DK / 8 + 2 * i + s, lane)};
+          const bf16x8 qt[1] = {record_frag(keys, (DK / 8 + 2 * c) * kB, 4 * i + s, 16 * lane)};
           dk[i] = mfma_parts(d1t, qt, dk[i]);
           dk[i] = mfma_parts(d2t, kt, dk[i]);
         }
       }
     }
-    // sum of P_ij over j < t <= i: prefix sums along 16 rows of each wavefront, added for the rows from t on
+    // sum of P_ij over j < t <= i: prefix sums along 8 rows of each wavefront, added for the rows from t on
     {
       float acc = 0.0f;
-#pragma unroll 4
-      for (int r = 0; r < 16; ++r) {
-        const int i = 16 * w + r;
+#pragma unroll 2
+      for (int r = 0; r < 8; ++r) {
+        const int i = 8 * wave + r;
         float v = sP[i * kPitch + lane];
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
@@ -527,12 +549,12 @@ __global__ __launch_bounds__(256) void k_delta_grads(GradArgs a) {
         const float before = __shfl_up(v, 1);
         if (lane > 0 && i >= lane) acc += before;
       }
-      sAcc[w][lane] = acc;
+      sAcc[wave][lane] = acc;
     }
     lds_barrier();
-    if (w == 0) {
+    if (wave == 0) {
       // sums of s over i >= t and of e over j < t
-      float v0 = sS0[lane], v1 = sS1[lane];
+      float v0 = sS0[0][lane] + sS0[1][lane], v1 = sS1[0][lane] + sS1[1][lane];
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) {
         const float down = __shfl_down(v0, d), up = __shfl_up(v1, d);
@@ -540,9 +562,10 @@ __global__ __launch_bounds__(256) void k_delta_grads(GradArgs a) {
         if (lane >= d) v1 += up;
       }
       const float before = __shfl_up(v1, 1);
-      const float last = sEg[C - 1];
-      float dg = ((sAcc[0][lane] + sAcc[1][lane]) + (sAcc[2][lane] + sAcc[3][lane])) + v0 + (lane > 0 ? before : 0.0f);
-      dg = fmaf(last, (sDot[0] + sDot[1]) + (sDot[2] + sDot[3]), dg);
+      float dg = v0 + (lane > 0 ? before : 0.0f), all = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dg += sAcc[i][lane], all += sDot[i];
+      dg = fmaf(sEg[C - 1], all, dg);
       float pa = 0.0f, pb = 0.0f;
       if (t0 + a.sh.place(lane) < L) {
         const int64_t t = (b * L + t0 + a.sh.place(lane)) * a.sh.heads + h;
@@ -567,7 +590,8 @@ __global__ __launch_bounds__(256) void k_delta_grads(GradArgs a) {
     for (int r = 0; r < 4; ++r) {
       const int64_t t = t0 + a.sh.place(16 * w + 4 * q4 + r);
       if (t < L) {
-        const int64_t to = ((b * L + t) * a.sh.hk + kh) * DK + state_row<ST>(i / ST, i % ST, l16);
+        const int tile = 2 * i + c;
+        const int64_t to = ((b * L + t) * a.sh.hk + kh) * DK + state_row<ST>(tile / ST, tile % ST, l16);
         bf16_t o;
         from_f32(dq[i][r], &o);
         a.dq[to] = o.bits;
@@ -607,8 +631,8 @@ void launch_rwalk(const RWalkArgs& a, int tiles, hipStream_t stream) {
 
 template <int DK>
 void launch_grads(const GradArgs& a, int64_t dv, dim3 grid, hipStream_t stream) {
-  if (dv == 64) hipLaunchKernelGGL((k_delta_grads<DK, 64>), grid, dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((k_delta_grads<DK, 128>), grid, dim3(256), 0, stream, a);
+  if (dv == 64) hipLaunchKernelGGL((k_delta_grads<DK, 64>), grid, dim3(512), 0, stream, a);
+  else hipLaunchKernelGGL((k_delta_grads<DK, 128>), grid, dim3(512), 0, stream, a);
 }
 
 }  // namespace

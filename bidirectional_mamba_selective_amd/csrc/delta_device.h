@@ -133,10 +133,6 @@ __device__ __forceinline__ int upper_at(int w, int s) { return w < 2 ? 2 * w + s
 __device__ __forceinline__ bool lower_has(int w, int s) { return s <= (w >> 1); }
 __device__ __forceinline__ bool upper_has(int w, int s) { return s >= (w >> 1); }
 
-__device__ __forceinline__ bf16x8 load_frag(const unsigned char* base, int frag, int lane) {
-  return *reinterpret_cast<const bf16x8*>(base + static_cast<size_t>(frag) * kFragBytes + lane * 16);
-}
-
 __device__ __forceinline__ void store_frag(unsigned char* base, int frag, int lane, bf16x8 v) {
   *reinterpret_cast<bf16x8*>(base + static_cast<size_t>(frag) * kFragBytes + lane * 16) = v;
 }

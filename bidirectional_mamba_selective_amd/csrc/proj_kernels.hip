@@ -171,9 +171,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_proj(Args a, int tiles_m, int 
     lds_barrier();
     const uint8_t *cx = sx[j & 1], *cw = sw[j & 1];
     Operand<WIDE> wf[NI], xf[2];
+    read_operand(cx + xlo, cx + xhi, 0, &xf[0]);
 #pragma unroll
     for (int n = 0; n < NI; ++n) read_operand(cw + wlo, cw + whi, n, &wf[n]);
-    read_operand(cx + xlo, cx + xhi, 0, &xf[0]);
     // a row tile's products are scaled, one by one, between those of the next; the pieces that came in during the last
     // step go into the other buffer, and those of the step after next are asked for, evenly over the step
     f32x4 t[NI];
