@@ -740,8 +740,9 @@ int bimamba_proj_fp8(const void* x, const float* x_scales, const void* w, const 
   if (rows <= 0 || d_out <= 0 || d_in <= 0) return BIMAMBA_ERR_INVALID_ARGUMENT;
   if (out_dtype != BIMAMBA_F32 && out_dtype != BIMAMBA_BF16) return BIMAMBA_ERR_UNSUPPORTED;
   if (d_in % 128 != 0 || d_out % 8 != 0) return BIMAMBA_ERR_UNSUPPORTED;
-  // tiles of 128 rows and 128 outputs go into a grid of 2^31 - 1 by 65535; byte counts stay below 2^53
-  if (d_out > (int64_t{1} << 22) || d_in > (int64_t{1} << 22) || rows > (int64_t{1} << 31))
+  // 256 rows or outputs lie within one buffer (2^31 - 1 bytes); a grid of tiles of 128 x 128 holds fewer than 2^32 threads
+  if (d_out > (int64_t{1} << 22) || d_in > (int64_t{1} << 22) || rows > (int64_t{1} << 31) ||
+      ((rows + 127) / 128) * ((d_out + 127) / 128) > (int64_t{1} << 23))
     return BIMAMBA_ERR_UNSUPPORTED;
   if (!x || !x_scales || !w || !w_scales || !out) return BIMAMBA_ERR_INVALID_ARGUMENT;
   const size_t kb = static_cast<size_t>(d_in) / 128;

@@ -453,11 +453,13 @@ int bimamba_adaln_bwd(const void* dout, const void* dres, const void* h, const v
  *   out[m,n] = sum_j x_scales[m,j] w_scales[n/128,j] sum_{k = 128 j}^{128 j + 127} x[m,k] w[n,k]
  * x and x_scales are what bimamba_adaln_fwd_fp8 writes (any row count: a batch of sequences, a block, one token); w is
  * quantised once, one scale for each 128 x 128 weights (n / 128 rounded down; the last row of scales serves the rest of
- * the outputs).  Products are exact, sums fp32, out is rounded to nearest even once.
+ * the outputs).  Products are exact and out is rounded to nearest even once; fp32 results sum in fp32, bf16 results as the
+ * 8-bit matrix instructions do, which drop low bits beside large terms (within 2^-12 of the terms' magnitudes, 1.4e-5
+ * normwise, before the rounding to bf16's 2^-9).
  *   x: [rows, d_in], w: [d_out, d_in], one byte a value; x_scales: [rows, d_in / 128] fp32;
  *   w_scales: [(d_out + 127) / 128, d_in / 128] fp32; out: [rows, d_out], out_dtype BIMAMBA_BF16 or BIMAMBA_F32.
- * Supported: d_in a multiple of 128, d_out of 8, both at most 2^22, 1 <= rows <= 2^31.  x, w and out 16-byte aligned,
- * scales 4.  out must not overlap an input.  No workspace. */
+ * Supported: d_in a multiple of 128, d_out of 8, both at most 2^22, 1 <= rows <= 2^31, and at most 2^23 tiles of 128 rows
+ * and 128 outputs.  x, w and out 16-byte aligned, scales 4.  out must not overlap an input.  No workspace. */
 int bimamba_proj_fp8(const void* x, const float* x_scales, const void* w, const float* w_scales, void* out,
                      int64_t rows, int64_t d_out, int64_t d_in, int out_dtype, hipStream_t stream);
 

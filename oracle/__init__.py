@@ -14,5 +14,6 @@ from .scan import (  # noqa: F401
     softplus,
 )
 from .conv import conv_anticausal, conv_bidir, conv_block, conv_causal  # noqa: F401
+from .delta import delta_bounds, delta_bwd, delta_fwd  # noqa: F401
 from .grads import adaln_bwd, adaln_fwd, conv_bwd, scan_bwd, scan_bwd_magnitudes  # noqa: F401
 from .ssd import ssd_discretise, ssd_forward_scan, ssd_reverse_scan, ssd_scan_block, ssd_scan_fwd  # noqa: F401
