@@ -64,10 +64,17 @@ template <int DK, bool GRAD>
 __global__ __launch_bounds__(256) void k_delta_prep(PrepArgs a) {
   constexpr int KS = DK / 32, ST = DK / 64;
   constexpr int kRow = DK + 8;
-  __shared__ float sN[C * kPitch], sT[C * kPitch], sA[C * kPitch];
+  // K's rows (then Q's, for their transposes), then N; A, then T: 34 KB, so that a compute unit holds four workgroups
+  // (68 KB, with arrays of their own: 50 us for 64 chunks of 32 heads of 128 x 128)
+  constexpr int kRows = C * kRow * 2 > C * kPitch * 4 ? C * kRow * 2 : C * kPitch * 4;
+  __shared__ __align__(16) unsigned char sKN[kRows];
+  __shared__ float sT[C * kPitch];
   __shared__ float sHi[C], sLo[C], sBeta[C];
-  __shared__ uint16_t sK[C * kRow];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, l16 = lane & 15, q4 = lane >> 4;
+  uint16_t* sK = reinterpret_cast<uint16_t*>(sKN);
+  float* sN = reinterpret_cast<float*>(sKN);
+  float* sA = sT;
+  const int lane = threadIdx.x & 63, l16 = lane & 15, q4 = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t ci = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int64_t share = a.sh.heads / a.sh.hk, kh = h / share, L = a.sh.L;
   const int64_t t0 = static_cast<int64_t>(a.sh.run(static_cast<int>(a.chunk0 + ci), a.chunks)) * C;
@@ -115,24 +122,89 @@ __global__ __launch_bounds__(256) void k_delta_prep(PrepArgs a) {
   lds_barrier();
 
   // scores of this wavefront's 16 rows against the tokens up to them
-  for (int j = 0; j <= w; ++j) {
-    f32x4 kk = zero4(), qk = zero4();
+  f32x4 kk[4], qk[4];
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const bf16x8 o = *reinterpret_cast<const bf16x8*>(sK + (16 * j + l16) * kRow + 32 * s + 8 * q4);
-      kk = mfma(kf[s], o, kk);
-      qk = mfma(qf[s], o, qk);
-    }
-    const int col = 16 * j + l16;
+  for (int j = 0; j < 4; ++j) {
+    kk[j] = qk[j] = zero4();
+    if (j <= w) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 16 * w + 4 * q4 + r;
-      const float d = col <= row ? ex((sHi[row] - sHi[col]) + (sLo[row] - sLo[col])) : 0.0f;
-      kk[r] = col < row ? kk[r] * d * sBeta[row] : 0.0f;
-      qk[r] = col <= row ? qk[r] * d * a.scale : 0.0f;
+      for (int s = 0; s < KS; ++s) {
+        const bf16x8 o = *reinterpret_cast<const bf16x8*>(sK + (16 * j + l16) * kRow + 32 * s + 8 * q4);
+        kk[j] = mfma(kf[s], o, kk[j]);
+        qk[j] = mfma(qf[s], o, qk[j]);
+      }
+      const int col = 16 * j + l16;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * w + 4 * q4 + r;
+        const float d = col <= row ? ex((sHi[row] - sHi[col]) + (sLo[row] - sLo[col])) : 0.0f;
+        kk[j][r] = col < row ? kk[j][r] * d * sBeta[row] : 0.0f;
+        qk[j][r] = col <= row ? qk[j][r] * d * a.scale : 0.0f;
+      }
     }
-    put_tile(sN, 16 * w, 16 * j, l16, q4, kk);
-    put_tile(sA, 16 * w, 16 * j, l16, q4, qk);
+  }
+  // K^T and Q^T once for the heads that share them
+  if (h % share == 0) {
+    unsigned char* key = a.keys + ((b * a.sh.hk + kh) * a.seg + ci) * a.lay.key_bytes;
+#pragma unroll
+    for (int which = 0; which < (GRAD ? 2 : 1); ++which) {
+      if (which == 1) {
+        lds_barrier();
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+          *reinterpret_cast<bf16x8*>(sK + (16 * w + l16) * kRow + 32 * s + 8 * q4) = qf[s];
+        lds_barrier();
+      }
+      for (int f = w; f < DK / 8; f += 4) {  // tile f / 2 of the state's rows, tokens 32 (f % 2)
+        const int col = state_row<ST>(f / (2 * ST), f / 2 % ST, l16);
+        union {
+          uint16_t u[8];
+          bf16x8 v;
+        } x;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x.u[e] = sK[(32 * (f & 1) + 8 * q4 + e) * kRow + col];
+        store_frag(key, which * (DK / 8) + f, lane, x.v);
+      }
+    }
+  }
+  lds_barrier();
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j <= w) {
+      put_tile(sN, 16 * w, 16 * j, l16, q4, kk[j]);
+      put_tile(sA, 16 * w, 16 * j, l16, q4, qk[j]);
+    }
+  lds_barrier();
+  // A's operands, before T takes its place
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int row = 16 * w + l16;
+    f32x8 m;
+    if constexpr (GRAD) {
+      if (upper_has(w, s)) {  // of its transpose
+        bf16x8 p[3];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int col = 32 * s + 8 * q4 + e;
+          m[e] = col >= row ? sA[col * kPitch + row] : 0.0f;
+        }
+        split8(m, p);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) store_frag(rec + a.lay.at, upper_at(w, s) * 3 + i, lane, p[i]);
+      }
+    } else {
+      if (lower_has(w, s)) {
+        bf16x8 p[2];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int col = 32 * s + 8 * q4 + e;
+          m[e] = col <= row ? sA[row * kPitch + col] : 0.0f;
+        }
+        split8(m, p);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) store_frag(rec + a.lay.a, lower_at(w, s) * 2 + i, lane, p[i]);
+      }
+    }
   }
   lds_barrier();
 
@@ -171,72 +243,31 @@ __global__ __launch_bounds__(256) void k_delta_prep(PrepArgs a) {
   }
   lds_barrier();
 
-  // operands of the walk
+  // T's operands
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
+    const int row = 16 * w + l16;
+    f32x8 t;
+    bf16x8 p[3];
     if (lower_has(w, s)) {
-      const int row = 16 * w + l16;
-      f32x8 t, m;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int col = 32 * s + 8 * q4 + e;
         t[e] = col <= row ? sT[row * kPitch + col] * sBeta[col] : 0.0f;
-        m[e] = col <= row ? sA[row * kPitch + col] : 0.0f;
       }
-      bf16x8 tp[3];
-      split8(t, tp);
+      split8(t, p);
 #pragma unroll
-      for (int i = 0; i < 3; ++i) store_frag(rec + a.lay.t, lower_at(w, s) * 3 + i, lane, tp[i]);
-      if constexpr (!GRAD) {
-        bf16x8 mp[2];
-        split8(m, mp);
+      for (int i = 0; i < 3; ++i) store_frag(rec + a.lay.t, lower_at(w, s) * 3 + i, lane, p[i]);
+    }
+    if (GRAD && upper_has(w, s)) {  // of its transpose
 #pragma unroll
-        for (int i = 0; i < 2; ++i) store_frag(rec + a.lay.a, lower_at(w, s) * 2 + i, lane, mp[i]);
+      for (int e = 0; e < 8; ++e) {
+        const int col = 32 * s + 8 * q4 + e;
+        t[e] = col >= row ? sT[col * kPitch + row] * sBeta[row] : 0.0f;
       }
-    }
-    if constexpr (GRAD) {
-      if (upper_has(w, s)) {
-        const int row = 16 * w + l16;  // the row of the transpose
-        f32x8 t, m;
+      split8(t, p);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int col = 32 * s + 8 * q4 + e;
-          t[e] = col >= row ? sT[col * kPitch + row] * sBeta[row] : 0.0f;
-          m[e] = col >= row ? sA[col * kPitch + row] : 0.0f;
-        }
-        bf16x8 tp[3], mp[3];
-        split8(t, tp);
-        split8(m, mp);
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          store_frag(rec + a.lay.tt, upper_at(w, s) * 3 + i, lane, tp[i]);
-          store_frag(rec + a.lay.at, upper_at(w, s) * 3 + i, lane, mp[i]);
-        }
-      }
-    }
-  }
-
-  // K^T and Q^T once for the heads that share them
-  if (h % share != 0) return;
-  unsigned char* key = a.keys + ((b * a.sh.hk + kh) * a.seg + ci) * a.lay.key_bytes;
-#pragma unroll
-  for (int which = 0; which < (GRAD ? 2 : 1); ++which) {
-    if (which == 1) {
-      lds_barrier();
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-        *reinterpret_cast<bf16x8*>(sK + (16 * w + l16) * kRow + 32 * s + 8 * q4) = qf[s];
-      lds_barrier();
-    }
-    for (int f = w; f < DK / 8; f += 4) {  // tile f / 2 of the state's rows, tokens 32 (f % 2)
-      const int col = state_row<ST>(f / (2 * ST), f / 2 % ST, l16);
-      union {
-        uint16_t u[8];
-        bf16x8 v;
-      } x;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x.u[e] = sK[(32 * (f & 1) + 8 * q4 + e) * kRow + col];
-      store_frag(key, which * (DK / 8) + f, lane, x.v);
+      for (int i = 0; i < 3; ++i) store_frag(rec + a.lay.tt, upper_at(w, s) * 3 + i, lane, p[i]);
     }
   }
 }
