@@ -343,17 +343,47 @@ __device__ __forceinline__ float sum_rows(float v) {
   return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
+// 32 columns of the states, of U and of dR as operands in LDS: rows of 64 bytes, their 16-byte chunks permuted so that 8 lanes
+// reading one chunk of 8 rows meet all banks.  Index in values.
+__device__ __forceinline__ int slice_at(int row, int chunk) { return row * 32 + ((chunk ^ ((row >> 1) & 3)) << 3); }
+
+template <int DK>
+struct Slices {
+  uint16_t s[3][DK * 32], ds[3][DK * 32], u[3][C * 32], r[3][C * 32];
+};
+
+struct Scores {
+  uint16_t d1[2][C * C], d1t[2][C * C], d2[2][C * C], d2t[2][C * C];
+};
+
+__device__ __forceinline__ void put_slice(uint16_t* to, int size, int at, f32x8 v) {
+  bf16x8 p[3];
+  split8(v, p);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) *reinterpret_cast<bf16x8*>(to + i * size + at) = p[i];
+}
+
+__device__ __forceinline__ void get_slice(const uint16_t* from, int size, int at, bf16x8 (&p)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) p[i] = *reinterpret_cast<const bf16x8*>(from + i * size + at);
+}
+
 // Eight wavefronts: wavefront w + 4 c takes the chunk's tokens 16 w .. + 15 and, of the tokens or columns that it meets
-// them with, the tiles of parity c.  What ends in an fp32 result (the sums of P, s and e) is formed from three parts of each
-// fp32 operand, D1 and D2 as operands of the bf16 results from two.
+// them with, the tiles of parity c.  The contractions over the value head's columns go 32 columns at a time: every value of
+// the states, U and dR is loaded once, a slice ahead, and split once into the three parts that all wavefronts read from
+// LDS.  What ends in an fp32 result (the sums of P, s and e) is formed from all three parts, D1 and D2 as operands of the
+// bf16 results from two.
 template <int DK, int DV>
 __global__ __launch_bounds__(512, 2) void k_delta_grads(GradArgs a) {
   constexpr int KS = DK / 32, ST = DK / 64, VS = DV / 32, KT = DK / 32, kRow = DK + 8, kPitch = C + 1;
-  __shared__ __align__(16) uint16_t sD1[2][C * C], sD1t[2][C * C], sD2[2][C * C], sD2t[2][C * C];
+  constexpr int kShared = sizeof(Slices<DK>) > sizeof(Scores) ? sizeof(Slices<DK>) : sizeof(Scores);
+  __shared__ __align__(16) unsigned char shared[kShared];  // the slices, then the scores
   __shared__ __align__(16) uint16_t sQ[C * kRow], sK[C * kRow];
   __shared__ float sP[C * kPitch];
   __shared__ __align__(16) float sHi[C], sLo[C], sEg[C], sKeep[C];
   __shared__ float sS0[2][C], sS1[2][C], sDb[C], sAcc[8][C], sDot[8];
+  Slices<DK>& sl = *reinterpret_cast<Slices<DK>*>(shared);
+  Scores& sc = *reinterpret_cast<Scores*>(shared);
   const int lane = threadIdx.x & 63, l16 = lane & 15, q4 = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave & 3, c = wave >> 2;
   const int64_t ci = blockIdx.x, kh = blockIdx.y, b = blockIdx.z, L = a.sh.L, share = a.sh.heads / a.sh.hk;
@@ -378,66 +408,63 @@ __global__ __launch_bounds__(512, 2) void k_delta_grads(GradArgs a) {
     lds_barrier();  // the previous head's readers of what is written here
     if (wave == 0) sEg[lane] = gates[lane], sKeep[lane] = gates[C + lane];
     if (wave == 1) sHi[lane] = gates[2 * C + lane], sLo[lane] = gates[3 * C + lane];
-    const float beta = gates[4 * C + 16 * w + l16];
-    const float rb = beta > 1e-30f ? 1.0f / beta : 0.0f;
-    // 32 columns of the value head at a time (not unrolled: brought forward, the loads of several do not fit the registers)
     f32x4 d1[2], d2[2], t1[KT], t2[KT], t3[KT];
-    float dot = 0.0f, ur = 0.0f;
+    float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < KT; ++i) t1[i] = t2[i] = t3[i] = zero4();
     d1[0] = d1[1] = d2[0] = d2[1] = zero4();
     const int val_pitch = static_cast<int>(a.sh.heads) * DV * 2;
     const __amdgpu_buffer_rsrc_t go = run_rows(a.dout + (b * L * a.sh.heads + h) * DV, a.sh, val_pitch, DV * 2, run);
-    const __amdgpu_buffer_rsrc_t gr = floats(a.drs + hc * C * DV, C * DV), gu = floats(a.us + hc * C * DV, C * DV);
     const __amdgpu_buffer_rsrc_t gs = floats(a.states + hc * DK * DV, DK * DV), gd = floats(a.dstates + hc * DK * DV, DK * DV);
+    // half of the workgroup brings U, the other dR
+    const __amdgpu_buffer_rsrc_t gur = floats((c ? a.drs : a.us) + hc * C * DV, C * DV);
     const int orow = a.sh.place(16 * w + l16) * val_pitch + 16 * q4;
-    const int urow = (l16 * DV + 8 * q4) * 4;  // of 16 rows of U or dR
-    int srow[KT];
-#pragma unroll
-    for (int i = 0; i < KT; ++i) srow[i] = (state_row<ST>((2 * i + c) / ST, (2 * i + c) % ST, l16) * DV + 8 * q4) * 4;
+    const int row = threadIdx.x >> 2, chunk = threadIdx.x & 3;  // of the states (DK 64: the first 256 threads')
+    const bool states = DK == 128 || c == 0;
+    const int at_state = (row * DV + 8 * chunk) * 4, at_ur = ((row & 63) * DV + 8 * chunk) * 4;
+    f32x8 st, ds, ur;
+    bf16x8 od[1], on;
+    auto fetch = [&](int s) {
+      if (states) st = load_f32x8(gs, at_state, 128 * s), ds = load_f32x8(gd, at_state, 128 * s);
+      ur = load_f32x8(gur, at_ur, 128 * s);
+      on = row_load8(go, orow + 64 * s);
+    };
+    fetch(0);
 #pragma unroll 1
     for (int s = 0; s < VS; ++s) {
-      bf16x8 rd[3], ud[3];
-      const bf16x8 od[1] = {row_load8(go, orow + 64 * s)};
-      const f32x8 r = load_f32x8(gr, urow + 64 * DV * w, 128 * s), u = load_f32x8(gu, urow + 64 * DV * w, 128 * s);
-      f32x8 st[2], ds[2];
-      st[0] = load_f32x8(gs, srow[0], 128 * s);
-      ds[0] = load_f32x8(gd, srow[0], 128 * s);
+      if (states) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ur = fmaf(u[e] * rb, r[e], ur);
-      split8(r, rd);
-      split8(u, ud);
+        for (int e = 0; e < 8; ++e) dot = fmaf(st[e], ds[e], dot);
+        put_slice(sl.s[0], DK * 32, slice_at(row, chunk), st);
+        put_slice(sl.ds[0], DK * 32, slice_at(row, chunk), ds);
+      }
+      put_slice(c ? sl.r[0] : sl.u[0], C * 32, slice_at(row & 63, chunk), ur);
+      od[0] = on;
+      fetch(s + 1 < VS ? s + 1 : s);
+      lds_barrier();
+      bf16x8 rd[3], ud[3];
+      get_slice(sl.r[0], C * 32, slice_at(16 * w + l16, q4), rd);
+      get_slice(sl.u[0], C * 32, slice_at(16 * w + l16, q4), ud);
 #pragma unroll
       for (int i = 0; i < KT; ++i) {
-        const f32x8 x = st[i & 1], z = ds[i & 1];
-        if (i + 1 < KT) {
-          st[(i + 1) & 1] = load_f32x8(gs, srow[i + 1], 128 * s);
-          ds[(i + 1) & 1] = load_f32x8(gd, srow[i + 1], 128 * s);
-        }
-        if (((KT == 4 ? i : 2 * (s & 1) + i) & 3) == w) {  // every value of the states in one wavefront
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dot = fmaf(x[e], z[e], dot);
-        }
+        const int at_row = slice_at(state_row<ST>((2 * i + c) / ST, (2 * i + c) % ST, l16), q4);
         bf16x8 y[3];
-        split8(x, y);
+        get_slice(sl.s[0], DK * 32, at_row, y);
         t1[i] = mfma_parts(od, y, t1[i]);
         t2[i] = mfma_parts(rd, y, t2[i]);
-        split8(z, y);
+        get_slice(sl.ds[0], DK * 32, at_row, y);
         t3[i] = mfma_parts(ud, y, t3[i]);
-        __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int jj = 0; jj < 2; ++jj)
         if (2 * jj + c <= w) {
           bf16x8 y[3];
-          split8(load_f32x8(gu, urow + 64 * DV * (2 * jj + c), 128 * s), y);
+          get_slice(sl.u[0], C * 32, slice_at(16 * (2 * jj + c) + l16, q4), y);
           d1[jj] = mfma_parts(od, y, d1[jj]);
           d2[jj] = mfma_parts(rd, y, d2[jj]);
         }
+      lds_barrier();
     }
-    ur = sum_rows(ur);
-    if (c == 0 && q4 == 0) sDb[16 * w + l16] = ur;
-    lds_barrier();
     const f32x4 eg = *reinterpret_cast<const f32x4*>(sEg + 16 * w + 4 * q4);
     const f32x4 keep = *reinterpret_cast<const f32x4*>(sKeep + 16 * w + 4 * q4);
 
@@ -461,6 +488,7 @@ __global__ __launch_bounds__(512, 2) void k_delta_grads(GradArgs a) {
           const int row = 16 * w + 4 * q4 + r;
           const float d = col <= row ? ex((sHi[row] - sHi[col]) + (sLo[row] - sLo[col])) : 0.0f;
           d1[jj][r] = col <= row ? d1[jj][r] * d * a.scale : 0.0f;
+          if (col == row) sDb[row] = d2[jj][r];  // dR_i.U_i
           d2[jj][r] = col < row ? -d2[jj][r] * d : 0.0f;
           pr[r] = col < row ? fmaf(d1[jj][r], qk[r], d2[jj][r] * kk[r]) : 0.0f;
         }
@@ -472,12 +500,12 @@ __global__ __launch_bounds__(512, 2) void k_delta_grads(GradArgs a) {
       split4(d2[jj], p2);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        write4<C>(sD1t[i], 16 * j + l16, 16 * w + 4 * q4, p1[i]);
-        write4<C>(sD2t[i], 16 * j + l16, 16 * w + 4 * q4, p2[i]);
+        write4<C>(sc.d1t[i], 16 * j + l16, 16 * w + 4 * q4, p1[i]);
+        write4<C>(sc.d2t[i], 16 * j + l16, 16 * w + 4 * q4, p2[i]);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          sD1[i][at<C>(16 * w + 4 * q4 + r, 16 * j + l16)] = static_cast<uint16_t>(p1[i][r >> 1] >> (16 * (r & 1)));
-          sD2[i][at<C>(16 * w + 4 * q4 + r, 16 * j + l16)] = static_cast<uint16_t>(p2[i][r >> 1] >> (16 * (r & 1)));
+          sc.d1[i][at<C>(16 * w + 4 * q4 + r, 16 * j + l16)] = static_cast<uint16_t>(p1[i][r >> 1] >> (16 * (r & 1)));
+          sc.d2[i][at<C>(16 * w + 4 * q4 + r, 16 * j + l16)] = static_cast<uint16_t>(p2[i][r >> 1] >> (16 * (r & 1)));
         }
       }
     }
@@ -515,10 +543,10 @@ __global__ __launch_bounds__(512, 2) void k_delta_grads(GradArgs a) {
       bf16x8 d1[2], d2[2], d1t[2], d2t[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        d1[i] = read8<C>(sD1[i], 16 * w + l16, 32 * s + 8 * q4);
-        d2[i] = read8<C>(sD2[i], 16 * w + l16, 32 * s + 8 * q4);
-        d1t[i] = read8<C>(sD1t[i], 16 * w + l16, 32 * s + 8 * q4);
-        d2t[i] = read8<C>(sD2t[i], 16 * w + l16, 32 * s + 8 * q4);
+        d1[i] = read8<C>(sc.d1[i], 16 * w + l16, 32 * s + 8 * q4);
+        d2[i] = read8<C>(sc.d2[i], 16 * w + l16, 32 * s + 8 * q4);
+        d1t[i] = read8<C>(sc.d1t[i], 16 * w + l16, 32 * s + 8 * q4);
+        d2t[i] = read8<C>(sc.d2t[i], 16 * w + l16, 32 * s + 8 * q4);
       }
 #pragma unroll
       for (int i = 0; i < KT; ++i) {
@@ -576,7 +604,9 @@ __global__ __launch_bounds__(512, 2) void k_delta_grads(GradArgs a) {
         bf16_t o;
         from_f32(ddt, &o);
         a.ddt[t] = o.bits;
-        from_f32(sDb[lane] * sigmoid_f32(-bf(a.b[t])), &o);
+        // (0 below 2^-60, where the product of two factors of beta leaves the range)
+        const float beta = gates[4 * C + lane];
+        from_f32(beta > 0x1p-60f ? sDb[lane] / beta * sigmoid_f32(-bf(a.b[t])) : 0.0f, &o);
         a.db[t] = o.bits;
       }
       pa = sum_rows(sum16(pa));
