@@ -754,9 +754,9 @@ def bimamba_adaln_fwd_fp8(x, gamma=None, beta=None, branch=None, post_weight=Non
         if branch is not None and h is None:
             h = torch.empty_like(x)
         if out is None:
-            out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+            out = torch.empty_like(x, dtype=torch.float8_e4m3fn)
         if scales is None:
-            scales = torch.empty((nb, L, nd // 128), dtype=torch.float32, device=dev)
+            scales = x.new_empty((nb, L, nd // 128), dtype=torch.float32)
         _check(h, "h", x.shape, x.dtype, dev)
         _check(out, "out", x.shape, torch.float8_e4m3fn, dev)
         _check(scales, "scales", (nb, L, nd // 128), torch.float32, dev)
@@ -815,7 +815,7 @@ def bimamba_proj_fp8(x, x_scales, w, w_scales, out=None, out_dtype=None, stream=
         _check(x_scales, "x_scales", (nb, L, k // 128), torch.float32, dev)
         _check(w_scales, "w_scales", ((n + 127) // 128, k // 128), torch.float32, dev)
         if out is None:
-            out = torch.empty((nb, L, n), dtype=out_dtype or torch.bfloat16, device=dev)
+            out = x.new_empty((nb, L, n), dtype=out_dtype or torch.bfloat16)
         _check(out, "out", (nb, L, n), out_dtype or out.dtype, dev)
         st = lib.bimamba_proj_fp8(_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), _ptr(out), nb * L, n, k,
                                   _io_dtype(out), _stream(stream, dev))
@@ -868,7 +868,8 @@ def bimamba_delta_fwd(q, k, v, dt, A, b, dt_bias=None, h_in=None, h_out=None, ou
         if out is None:
             out = torch.empty_like(v)
         _check(out, "out", v.shape, v.dtype, dev)
-        workspace, wbytes = _workspace(workspace, lib.bimamba_delta_fwd_workspace_bytes(nb, L, hk, nh, dk, dv), dev)
+        need = lib.bimamba_delta_fwd_workspace_bytes(nb, L, hk, nh, dk, dv)
+        workspace, wbytes = (None, 0) if workspace is None and need == 0 else _workspace(workspace, need, dev)
         st = lib.bimamba_delta_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A), _ptr(b), _ptr(dt_bias), _ptr(h_in),
                                    _ptr(h_out), _ptr(out), nb, L, hk, nh, dk, dv, dk ** -0.5 if scale is None else scale,
                                    _io_dtype(q), flags, _ptr(workspace), wbytes, _stream(stream, dev))
