@@ -343,6 +343,18 @@ __device__ __forceinline__ float sum_rows(float v) {
   return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
+// Sum over lanes 0 .. l, by shifts within rows of 16 lanes and broadcasts from row to row.
+__device__ __forceinline__ float prefix_sum(float v) {
+  v = add_dpp<0x111>(v);  // row_shr:1, 2, 4, 8
+  v = add_dpp<0x112>(v);
+  v = add_dpp<0x114>(v);
+  v = add_dpp<0x118>(v);
+  // the last lane of rows 0 and 2 to the rows after them, then lane 31 to rows 2 and 3
+  v += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x142, 0xa, 0xf, true));
+  v += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x143, 0xc, 0xf, true));
+  return v;
+}
+
 // 32 columns of the states, of U and of dR as operands in LDS: rows of 64 bytes, their 16-byte chunks permuted so that 8 lanes
 // reading one chunk of 8 rows meet all banks.  Index in values.
 __device__ __forceinline__ int slice_at(int row, int chunk) { return row * 32 + ((chunk ^ ((row >> 1) & 3)) << 3); }
@@ -381,7 +393,7 @@ __global__ __launch_bounds__(512, 2) void k_delta_grads(GradArgs a) {
   __shared__ __align__(16) uint16_t sQ[C * kRow], sK[C * kRow];
   __shared__ float sP[C * kPitch];
   __shared__ __align__(16) float sHi[C], sLo[C], sEg[C], sKeep[C];
-  __shared__ float sS0[2][C], sS1[2][C], sDb[C], sAcc[8][C], sDot[8];
+  __shared__ float sS0[2][C], sS1[2][C], sDb[C], sTurn[C], sAcc[8][C], sDot[8];
   Slices<DK>& sl = *reinterpret_cast<Slices<DK>*>(shared);
   Scores& sc = *reinterpret_cast<Scores*>(shared);
   const int lane = threadIdx.x & 63, l16 = lane & 15, q4 = lane >> 4;
@@ -407,6 +419,12 @@ __global__ __launch_bounds__(512, 2) void k_delta_grads(GradArgs a) {
     const float* gates = reinterpret_cast<const float*>(a.heads + hc * a.lay.bytes);
     lds_barrier();  // the previous head's readers of what is written here
     if (wave == 0) sEg[lane] = gates[lane], sKeep[lane] = gates[C + lane];
+    // what the last step takes: this lane's token
+    const bool real = t0 + a.sh.place(lane) < L;
+    const int64_t t_own = (b * L + (real ? t0 + a.sh.place(lane) : L - 1)) * a.sh.heads + h;
+    uint16_t own_dt = 0, own_b = 0;
+    float own_beta = 0.0f;
+    if (wave == 0) own_dt = a.dt[t_own], own_b = a.b[t_own], own_beta = gates[4 * C + lane];
     if (wave == 1) sHi[lane] = gates[2 * C + lane], sLo[lane] = gates[3 * C + lane];
     f32x4 d1[2], d2[2], t1[KT], t2[KT], t3[KT];
     float dot = 0.0f;
@@ -565,49 +583,36 @@ __global__ __launch_bounds__(512, 2) void k_delta_grads(GradArgs a) {
     // sum of P_ij over j < t <= i: prefix sums along 8 rows of each wavefront, added for the rows from t on
     {
       float acc = 0.0f;
-#pragma unroll 2
+#pragma unroll
       for (int r = 0; r < 8; ++r) {
         const int i = 8 * wave + r;
-        float v = sP[i * kPitch + lane];
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-          const float up = __shfl_up(v, d);
-          if (lane >= d) v += up;
-        }
-        const float before = __shfl_up(v, 1);
-        if (lane > 0 && i >= lane) acc += before;
+        const float before = prefix_sum(lane > 0 ? sP[i * kPitch + lane - 1] : 0.0f);
+        acc += i >= lane ? before : 0.0f;
       }
       sAcc[wave][lane] = acc;
     }
     lds_barrier();
     if (wave == 0) {
-      // sums of s over i >= t and of e over j < t
-      float v0 = sS0[0][lane] + sS0[1][lane], v1 = sS1[0][lane] + sS1[1][lane];
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) {
-        const float down = __shfl_down(v0, d), up = __shfl_up(v1, d);
-        if (lane + d < 64) v0 += down;
-        if (lane >= d) v1 += up;
-      }
-      const float before = __shfl_up(v1, 1);
-      float dg = v0 + (lane > 0 ? before : 0.0f), all = 0.0f;
+      // sums of s over i >= t (as prefix sums of the reversed row) and of e over j < t
+      const float from = prefix_sum(sS0[0][C - 1 - lane] + sS0[1][C - 1 - lane]);
+      const float before = prefix_sum(lane > 0 ? sS1[0][lane - 1] + sS1[1][lane - 1] : 0.0f);
+      sTurn[C - 1 - lane] = from;
+      float dg = sTurn[lane] + before, all = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) dg += sAcc[i][lane], all += sDot[i];
       dg = fmaf(sEg[C - 1], all, dg);
       float pa = 0.0f, pb = 0.0f;
-      if (t0 + a.sh.place(lane) < L) {
-        const int64_t t = (b * L + t0 + a.sh.place(lane)) * a.sh.heads + h;
-        const float x = bf(a.dt[t]) + (a.dt_bias ? a.dt_bias[h] : 0.0f);
+      if (real) {
+        const float x = bf(own_dt) + (a.dt_bias ? a.dt_bias[h] : 0.0f);
         const float ddt = dg * a.A[h] * sigmoid_f32(x);
         pa = dg * softplus_f32(x);
         pb = ddt;
         bf16_t o;
         from_f32(ddt, &o);
-        a.ddt[t] = o.bits;
+        a.ddt[t_own] = o.bits;
         // (0 below 2^-60, where the product of two factors of beta leaves the range)
-        const float beta = gates[4 * C + lane];
-        from_f32(beta > 0x1p-60f ? sDb[lane] / beta * sigmoid_f32(-bf(a.b[t])) : 0.0f, &o);
-        a.db[t] = o.bits;
+        from_f32(own_beta > 0x1p-60f ? sDb[lane] / own_beta * sigmoid_f32(-bf(own_b)) : 0.0f, &o);
+        a.db[t_own] = o.bits;
       }
       pa = sum_rows(sum16(pa));
       pb = sum_rows(sum16(pb));
