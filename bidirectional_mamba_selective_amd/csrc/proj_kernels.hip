@@ -269,20 +269,37 @@ void launch_tiles(const Args& a, hipStream_t stream) {
                      static_cast<int>(tn));
 }
 
+template <typename T, bool WIDE, int MI>
+void launch_rows(const Args& a, hipStream_t stream) {
+  hipLaunchKernelGGL((k_proj_rows<T, WIDE, MI>), dim3(static_cast<unsigned>((a.n + 15) / 16)), dim3(512), 0, stream, a);
+}
+
+// Which kernel, by the groups of 16 rows times the outputs and by the tiles of each size (us a call, k = 4096 unless
+// given; bf16 | fp32 results):
+// - k_proj_rows reads every row again for each 16 outputs, tiles of 64 x 64 walk all of k one after the other.  Rows for
+//   groups x n <= 8192 and 32 rows (fp32, whose tiles are slower: 16384 and 64), rows and tiles at
+//     16 x 4096: 7.2, 14.2 | 7.2, 18.5       32 x 4096: 10.4, 14.1 | 10.2, 18.7     16 x 8192: 12.1, 14.7 | 12.2, 19.4
+//     32 x 8192: 17.5, 14.9 | 17.2, 19.4     64 x 4096: 16.3, 14.5 | 16.4, 19.0     16 x 16384: 22.4, 15.7 | 22.5, 20.1
+// - 128 x 128 from more than 192 of them, below that too few compute units have one; 64 x 64 and 128 x 128 at
+//     768 x 4096 (192): 41.9, 42.2 | 48.8, 52.0       896 x 4096 (224): 50.4, 41.9 | 58.0, 53.4
+//     768 x 4096, k = 1024: 11.7, 13.3 | 14.6, 17.3   896 x 4096: 14.1, 13.5 | 17.5, 17.8
+// - 256 x 256 from more than 128 of them; 128 x 128 and 256 x 256 at
+//     2048 x 4096 (128): 61.7, 62.8       2304 x 4096 (144): 88.5, 59.9       4096 x 4096 (256): 109.3, 70.6
+//     2048 x 4096, k = 1024: 19.9, 24.4   2560 x 4096 (160): 29.9, 25.0       5120 x 4096 (320): 45.2, 44.8
+//   The operands of fp32 results, widened, do not fit the registers of such a tile.
 template <typename T, bool WIDE>
 void launch_typed(const Args& a, hipStream_t stream) {
-  if (a.m <= 64) {
-    const dim3 grid(static_cast<unsigned>((a.n + 15) / 16));
-    if (a.m <= 16) hipLaunchKernelGGL((k_proj_rows<T, WIDE, 1>), grid, dim3(512), 0, stream, a);
-    else if (a.m <= 32) hipLaunchKernelGGL((k_proj_rows<T, WIDE, 2>), grid, dim3(512), 0, stream, a);
-    else hipLaunchKernelGGL((k_proj_rows<T, WIDE, 4>), grid, dim3(512), 0, stream, a);
-    return;
+  const int64_t groups = (a.m + 15) / 16;
+  if (a.m <= (WIDE ? 64 : 32) && groups * a.n <= (WIDE ? 16384 : 8192)) {
+    if (groups == 1) return launch_rows<T, WIDE, 1>(a, stream);
+    if (groups == 2) return launch_rows<T, WIDE, 2>(a, stream);
+    if constexpr (WIDE) return launch_rows<T, WIDE, 4>(a, stream);
   }
   const int64_t t128 = (a.m + 127) / 128 * ((a.n + 127) / 128), t256 = (a.m + 255) / 256 * ((a.n + 255) / 256);
   if constexpr (!WIDE) {
-    if (t256 >= 512) return launch_tiles<T, WIDE, 8, 4, 2, 4>(a, stream);
+    if (t256 > 128) return launch_tiles<T, WIDE, 8, 4, 2, 4>(a, stream);
   }
-  if (t128 >= 512) launch_tiles<T, WIDE, 4, 4, 2, 2>(a, stream);
+  if (t128 > 192) launch_tiles<T, WIDE, 4, 4, 2, 2>(a, stream);
   else launch_tiles<T, WIDE, 2, 2, 2, 2>(a, stream);
 }
 

@@ -149,7 +149,7 @@ def test_proj_shapes(m, n, k):
     check_proj(m, n, k, torch.float32, seed=m + 1)
 
 
-@pytest.mark.parametrize("m,n,k", [(4000, 2056, 128), (2049, 4104, 384), (8200, 4096, 256)])
+@pytest.mark.parametrize("m,n,k", [(2000, 2056, 384), (4000, 2056, 128), (2049, 4104, 384), (8200, 4096, 256)])
 def test_proj_large_tiles(m, n, k):
     """The tiles of 128 and 256 rows, with ragged edges and an odd and an even number of blocks."""
     torch = torch_mod()
