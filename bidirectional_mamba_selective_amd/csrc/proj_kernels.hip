@@ -101,8 +101,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rows(const uint8_t* p, in
 
 // Tiles of WM x WN wavefronts of 16 MI rows x 16 NI outputs (16 NI divides 128, so a wavefront's outputs share their
 // scales).  Two LDS buffers and one barrier per step of 128 inputs: rows are loaded into registers two steps ahead and
-// written to the other buffer one step ahead, in pieces that are spread over the step's products (all at once, as a burst
-// of every wavefront, the loads took longer than a step: 626 us at 16384 x 8192 x 4096).
+// written to the other buffer one step ahead, in pieces that are spread over the step's products.  Measured at 16384 x
+// 8192 x 4096, bf16 results: 565 to 600 us with the clock (1.85 to 1.95 PFLOP/s; the library's 8-bit product with a
+// single scale reaches 2.49 on 8192^3); loads in one burst at the step's start 626, straight into LDS slower (later LDS
+// reads wait for them), two row tiles read ahead 802 (spills).  What bounds it: after each barrier the matrix cores wait for
+// the first operands from LDS, and 16 fp32 multiply-adds a product apply the scales.  fp32 results are bound by the
+// widening to bf16, done again by each wavefront that reads an operand: 1001 x 1920 x 3840 in 28 us.
 template <typename T, bool WIDE, int MI, int NI, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_proj(Args a, int tiles_m, int tiles_n) {
   constexpr int W = WM * WN, BM = 16 * MI * WM, BN = 16 * NI * WN, LX = BM / 8 / W, LW = BN / 8 / W;
@@ -211,7 +215,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_proj(Args a, int tiles_m, int 
 }
 
 // Few rows: the weights pass through once and bound the call.  A workgroup takes 16 outputs of all rows (16 MI of them); its
-// eight wavefronts take every eighth block of inputs, straight into registers, and add their sums in LDS.
+// eight wavefronts take every eighth block of inputs, straight into registers, and add their sums in LDS.  What bounds it
+// beside the weights (16 rows x 4096 x 4096: 7.2 us, 2.3 TB/s) is reading the rows again for each 16 outputs, from the L2.
 template <typename T, bool WIDE, int MI>
 __global__ __launch_bounds__(512) void k_proj_rows(Args a) {
   constexpr int W = 8;

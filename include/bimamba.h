@@ -472,10 +472,10 @@ int bimamba_proj_fp8(const void* x, const float* x_scales, const void* w, const 
  *   (the state before the first token is h_in, or zeros)
  * Layouts: q, k [batch, seqlen, nheads_k, headdim_k]; v, out [batch, seqlen, nheads, headdim_v]; dt, b [batch, seqlen,
  * nheads]; A, dt_bias [nheads] fp32; h_in, h_out [batch, nheads, headdim_k, headdim_v] fp32, the state before the
- * direction's first and after its last token (the cache of block decoding: a block, or a single token, is a call with both; h_out may
- * equal h_in).  dt_bias, h_in and h_out may be NULL (zeros; not written).
- * The layer is meant for A <= 0 and keys of about unit length; the states grow without bound otherwise.  Decays below e^-256 per token
- * count as e^-256 (zero in fp32).  b = -inf and dt = -inf are allowed and make a token that leaves the state as it is
+ * direction's first and after its last token (the cache of block decoding: a block, or a single token, is a call
+ * with both; h_out may equal h_in).  dt_bias, h_in and h_out may be NULL (zeros; not written).
+ * The layer is meant for A <= 0 and keys of about unit length; the states grow without bound otherwise.  Decays below
+ * e^-256 per token count as e^-256 (zero in fp32).  b = -inf and dt = -inf are allowed and make a token that leaves the state as it is
  * (a padded place: with finite q, k, v there); other non-finite values make the results of their batch element and head
  * non-finite from the 64-token chunk on in which they stand.
  * Supported: io_dtype BIMAMBA_BF16 (q, k, v, dt, b, out), headdim_k and headdim_v 64 or 128, nheads a multiple of
@@ -496,7 +496,8 @@ int bimamba_delta_fwd(const void* q, const void* k, const void* v, const void* d
  * h_out (NULL = 0).  Nothing of the forward call is needed: everything is recomputed from its inputs.
  *   dq, dk, dv, ddt, db: like their inputs (bf16, rounded once; dq and dk summed over the heads that share them);
  *   dA, ddt_bias [nheads] fp32, summed over batch and tokens; dh_in: the gradient of h_in.
- * ddt_bias and dh_in may be NULL (not written); they may be asked for also where dt_bias or h_in is NULL.  dh_in may
+ * db is 0 where beta is below 2^-60.  ddt_bias and dh_in may be NULL (not written); they may be asked for also where
+ * dt_bias or h_in is NULL.  dh_in may
  * equal dh_out.  All sums run in a fixed order: two calls on the same inputs give the same bits.  Shapes, types, flags and
  * alignment are as for bimamba_delta_fwd; workspace 256-byte aligned, contents ignored on entry.  No output may overlap
  * an input (dh_in equal to dh_out excepted), another output or the workspace. */
