@@ -411,7 +411,7 @@ int bimamba_adaln_fwd(const void* x, const void* branch, const float* post_weigh
 /* bimamba_adaln_fwd with out in 8 bits, as the projection that follows it reads it (bimamba_proj_fp8): with
  * y the value that bimamba_adaln_fwd rounds to out, and for each row and each run of 128 columns
  *   scale = max(max |y|, 2^-100) / 448,   out = y / scale rounded to nearest even e4m3
- * (OCP e4m3: 448 is its largest value; y / scale is formed as y * (1 / scale)).  With beta NULL and RMS_NORM this is the
+ * (OCP e4m3: 448 is its largest value; both divisions are fp32 ones, correctly rounded).  With beta NULL and RMS_NORM this is the
  * root-mean-square norm behind the residual's addition.
  *   out: [batch, seqlen, d_model], one byte a value; scales: [batch, seqlen, d_model / 128] fp32.
  * A NaN makes out NaN where bimamba_adaln_fwd's would be one; the scales pass over it.
