@@ -11,9 +11,9 @@
 //
 // k_delta_prep forms T, A, the decays and K^T of all chunks at once; k_delta_walk then goes over the chunks with the state
 // in fp32 registers, a workgroup per head and 16 or 32 columns of it (the columns of S, U, V and O are independent).
-// Products run on the matrix cores with bf16 operands and fp32 sums.  q, k and v are bf16 already; S, U and T are taken
-// as three bf16 parts (24 bits), so a state keeps fp32 accuracy over any number of chunks; A and the copies of S and U
-// that only the bf16 output sees, as two.
+// Products run on the matrix cores with bf16 operands and fp32 sums.  q, k and v are bf16 already; S, U, T and A are taken
+// as three bf16 parts (24 bits): a state keeps fp32 accuracy over any number of chunks, and out's terms have it when
+// their sum is rounded.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -60,15 +60,16 @@ __device__ __forceinline__ f32x4 tile_product(const float* x, int row0, int k0, 
 
 // One workgroup per (chunk, head, batch element); all chunks are independent.  N and A are two products of the chunk's
 // rows; (I + N)^-1 is built from its four 16 x 16 diagonal blocks, inverted by substitution, and products of blocks, in
-// fp32 matrix instructions.  Bound by the latency of that chain of small products and the LDS between them: 64 chunks of
-// 32 heads of 128 x 128 take 42 us, 96 MB written to the last-level cache, a quarter of the call.  The record's gates: e^g, e^(g_C - g), g as two floats whose sum carries
-// it to 2^-48 (differences of g stay exact to fp32 however far the chunk has decayed), beta; 64 of each.
+// fp32 matrix instructions.  Bound by the latency of that chain of small products and the LDS between them: 57 chunks of
+// 32 heads of 128 x 128 take 40 us, 99 MB written to the last-level cache, a quarter of the call.  The record's gates:
+// e^g, e^(g_C - g), g as two floats whose sum carries it to 2^-48 (differences of g stay exact to fp32 however far the
+// chunk has decayed), beta; 64 of each.
 template <int DK, bool GRAD>
 __global__ __launch_bounds__(256) void k_delta_prep(PrepArgs a) {
   constexpr int KS = DK / 32, ST = DK / 64;
   constexpr int kRow = DK + 8;
   // K's rows (then Q's, for their transposes), then N; A, then T: 34 KB, so that a compute unit holds four workgroups
-  // (68 KB, with arrays of their own: 50 us for 64 chunks of 32 heads of 128 x 128)
+  // (68 KB, with arrays of their own, took a fifth longer)
   constexpr int kRows = C * kRow * 2 > C * kPitch * 4 ? C * kRow * 2 : C * kPitch * 4;
   __shared__ __align__(16) unsigned char sKN[kRows];
   __shared__ float sT[C * kPitch];
@@ -197,7 +198,7 @@ __global__ __launch_bounds__(256) void k_delta_prep(PrepArgs a) {
       }
     } else {
       if (lower_has(w, s)) {
-        bf16x8 p[2];
+        bf16x8 p[3];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int col = 32 * s + 8 * q4 + e;
@@ -205,7 +206,7 @@ __global__ __launch_bounds__(256) void k_delta_prep(PrepArgs a) {
         }
         split8(m, p);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) store_frag(rec + a.lay.a, lower_at(w, s) * 2 + i, lane, p[i]);
+        for (int i = 0; i < 3; ++i) store_frag(rec + a.lay.a, lower_at(w, s) * 3 + i, lane, p[i]);
       }
     }
   }
@@ -310,18 +311,20 @@ __device__ __forceinline__ bool place(int64_t slices, int64_t rows, int64_t* row
 //   K^T U: through LDS, the wavefront's rows of S
 // What bounds it is the latency of one chunk's chain, which no other chunk can shorten: three LDS round trips of 140 to 185
 // cycles, three barriers, the products between them and the three-part splits; 2.0 us a chunk at 32 heads of 128 x 128
-// (64 chunks in 130 us; 65536 tokens, with k_delta_prep, in 2.70 ms, where the inputs' bytes take 0.43).  16 columns
+// (57 chunks in 115 us; 65536 tokens, with k_delta_prep, in 2.65 ms, where the inputs' bytes take 0.43).  16 columns
 // a workgroup put one on every compute unit at 32 heads.  The whole chain in the registers of one wavefront, without
-// barriers, took 166 us: its vector instructions, no longer spread over four SIMDs, then set the pace.
-// Four more take the products that only the output needs (Q S, A U) between the same barriers; without an output (SAVE)
-// there are none.  The next chunk's operands are loaded into the registers of the current chunk's as soon as these have
-// been used.
+// barriers, took 166 us where this took 130: its vector instructions, no longer spread over four SIMDs, then set the
+// pace.
+// Four more take the products that only the output needs (Q S, A U) between the same barriers, where the main ones leave
+// the matrix cores free: one part of S behind the first barrier, two behind the second (all three behind the first: 2.96
+// ms), the query rows asked for a chunk ahead (2.78 ms otherwise).  Without an output (SAVE) there are none.  The next
+// chunk's other operands are loaded into the registers of the current chunk's as soon as these have been used.
 template <int DK, int NT, bool SAVE>
 __global__ __launch_bounds__(SAVE ? 256 : 512, SAVE ? 1 : 2) void k_delta_walk(WalkArgs a) {
   constexpr int KS = DK / 32, ST = DK / 64, NS = 16 * NT, kB = static_cast<int>(kFragBytes);
   typedef typename Own<ST>::type own_t;
   __shared__ __align__(16) float sP[NT][4][4][256];
-  __shared__ __align__(16) uint16_t sS[2][NS * DK], sR[3][NS * C], sU[3][NS * C], sV[2][NS * C];
+  __shared__ __align__(16) uint16_t sS[3][NS * DK], sR[3][NS * C], sU[3][NS * C], sV[3][NS * C];
   const int lane = threadIdx.x & 63, l16 = lane & 15, q4 = lane >> 4, lane16 = lane * 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave & 3;
   int64_t bh, slice;
@@ -343,12 +346,12 @@ __global__ __launch_bounds__(SAVE ? 256 : 512, SAVE ? 1 : 2) void k_delta_walk(W
     const uint16_t* q0 = a.q + (b * a.sh.L * a.sh.hk + kh) * DK;
     uint16_t* out0 = a.out + (b * a.sh.L * a.sh.heads + h) * dv + n0;
     const int key_row = a.sh.place(16 * w + l16) * key_pitch + 16 * q4;
-    bf16x8 qf[KS], af[2][2];
+    bf16x8 qf[KS], qn[KS], af[2][3];
     f32x4 eg;
     auto load_q = [&](int ci) {
       const __amdgpu_buffer_rsrc_t q = run_rows(q0, a.sh, key_pitch, DK * 2, a.sh.run(a.first + ci, a.all));
 #pragma unroll
-      for (int s = 0; s < KS; ++s) qf[s] = row_load8(q, key_row + 64 * s);
+      for (int s = 0; s < KS; ++s) qn[s] = row_load8(q, key_row + 64 * s);
     };
     auto load_eg = [&]() { eg = gates4(record(rec, a.lay.bytes), 0); };
     auto load_a = [&]() {
@@ -357,44 +360,48 @@ __global__ __launch_bounds__(SAVE ? 256 : 512, SAVE ? 1 : 2) void k_delta_walk(W
       for (int s = 0; s < 2; ++s)
         if (lower_has(w, s))
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            af[s][i] = record_frag(r, static_cast<int>(a.lay.a) + lower_at(w, s) * 2 * kB, i, lane16);
+          for (int i = 0; i < 3; ++i)
+            af[s][i] = record_frag(r, static_cast<int>(a.lay.a) + lower_at(w, s) * 3 * kB, i, lane16);
     };
     load_q(0), load_eg(), load_a();
     for (int ci = 0; ci < chunks; ++ci) {
       const int next = ci + 1 < chunks ? ci + 1 : ci;
-      lds_barrier();
-      f32x4 o[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        o[nt][0] = o[nt][1] = zero4();
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            o[nt][i] = mfma(qf[s], read8<DK>(sS[i], 16 * nt + l16, 32 * s + 8 * q4), o[nt][i]);
-      }
+      for (int s = 0; s < KS; ++s) qf[s] = qn[s];
       load_q(next);
       lds_barrier();
+      // sS holds until the chunk's last barrier
+      f32x4 o[NT][3];
+      auto read_state = [&](int i) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) o[nt][0] = (o[nt][0] + o[nt][1]) * (eg * a.scale);
+        for (int nt = 0; nt < NT; ++nt) {
+          o[nt][i] = zero4();
+#pragma unroll
+          for (int s = 0; s < KS; ++s)
+            o[nt][i] = mfma(qf[s], read8<DK>(sS[i], 16 * nt + l16, 32 * s + 8 * q4), o[nt][i]);
+        }
+      };
+      read_state(0);
+      lds_barrier();
+      read_state(1), read_state(2);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) o[nt][0] = sum3(o[nt]) * (eg * a.scale);
       if (next > ci) rec += rec_bytes;
       load_eg();
       lds_barrier();
       const __amdgpu_buffer_rsrc_t out = run_rows(out0, a.sh, val_pitch, 2 * NS, a.sh.run(a.first + ci, a.all));
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        f32x4 low = zero4();
+        o[nt][1] = o[nt][2] = zero4();
 #pragma unroll
         for (int s = 0; s < 2; ++s)
           if (lower_has(w, s)) {
-            const bf16x8 hi = read8<C>(sV[0], 16 * nt + l16, 32 * s + 8 * q4);
-            const bf16x8 lo = read8<C>(sV[1], 16 * nt + l16, 32 * s + 8 * q4);
-            low = mfma(af[s][1], hi, low);
-            o[nt][0] = mfma(af[s][0], hi, o[nt][0]);
-            low = mfma(af[s][0], lo, low);
+            bf16x8 y[3];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) y[i] = read8<C>(sV[i], 16 * nt + l16, 32 * s + 8 * q4);
+            mfma_three(af[s], y, o[nt]);
           }
-        o[nt][0] += low;
+        o[nt][0] = sum3(o[nt]);
       }
       load_a();
 #pragma unroll
@@ -486,7 +493,7 @@ __global__ __launch_bounds__(SAVE ? 256 : 512, SAVE ? 1 : 2) void k_delta_walk(W
           for (int r = 0; r < 4; ++r) to[(4 * st + r) * dv] = S[st][nt][r];
       } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 3; ++i)
           *reinterpret_cast<own_t*>(sS[i] + at<DK>(16 * nt + l16, state_row<ST>(w, 0, 4 * q4))) = own[i];
       }
     }
@@ -535,10 +542,10 @@ __global__ __launch_bounds__(SAVE ? 256 : 512, SAVE ? 1 : 2) void k_delta_walk(W
 #pragma unroll
         for (int r = 0; r < 4; ++r) to[r * dv] = U[nt][r];
       } else {
-        u32x2 o[2];
+        u32x2 o[3];
         split4(U[nt], o);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) write4<C>(sV[i], 16 * nt + l16, 16 * w + 4 * q4, o[i]);
+        for (int i = 0; i < 3; ++i) write4<C>(sV[i], 16 * nt + l16, 16 * w + 4 * q4, o[i]);
       }
     }
     const float decay = last;

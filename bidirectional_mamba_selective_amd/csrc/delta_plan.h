@@ -33,7 +33,7 @@ inline Layout make_layout(int64_t dk, bool grad) {
     l.tt = off, off += kTriFrags * 3 * kFragBytes;
     l.at = off, off += kTriFrags * 3 * kFragBytes;
   } else {
-    l.a = off, off += kTriFrags * 2 * kFragBytes;
+    l.a = off, off += kTriFrags * 3 * kFragBytes;
   }
   l.bytes = align256(off);
   l.key_bytes = static_cast<size_t>(dk / 16) * 2 * kFragBytes * (grad ? 2 : 1);
@@ -41,9 +41,9 @@ inline Layout make_layout(int64_t dk, bool grad) {
 }
 
 // Columns of a value head that one workgroup of a walk takes, in tiles of 16.  While 16 each give every compute unit at most
-// one workgroup a step is latency, and narrower is faster (32 heads of 128 columns: 65536 tokens forward in 2.73 ms with
-// 16, 3.20 with 32; 4096 tokens backward 0.76 and 0.83); beyond that what a step reads is shared by more columns (64
-// heads: 4096 tokens forward 0.36 ms with 16, 0.27 with 32; 2048 backward 0.76 and 0.65; 128 heads 0.71 and 0.52).
+// one workgroup a step is latency, and narrower is faster (32 heads of 128 columns, 4096 tokens: forward 188 us with 16,
+// 205 with 32; backward 722 and 786); beyond that what a step reads is shared by more columns (64 heads: 4096 tokens
+// forward 355 us with 16, 273 with 32; 2048 backward 720 and 607; 128 heads 700 and 525, 1400 and 1156).
 inline int walk_tiles(int64_t heads, int64_t dv) {
   return heads * (dv / 16) <= 256 ? 1 : 2;
 }
@@ -56,9 +56,9 @@ struct Plan {
 };
 
 // Forward: the operands of `seg` chunks of every head at a time, so that they are read from the last-level cache (256 MiB)
-// rather than from memory; the states between two segments.  Segments of 32, 64, 96, 160 and 224 MiB: 65536 tokens of 32
-// heads of 128 x 128 in 3.06, 2.81, 2.74, 3.09 and 3.18 ms (all at once: 2.99), 16384 tokens in 779, 711, 683, 712 and 807
-// us (785), 4 x 8192 tokens in 1.09, 1.10, 1.08, 1.15 and 1.15 ms (1.06).
+// rather than from memory; the states between two segments.  Segments of 32, 64, 96, 128 and 160 MiB: 65536 tokens of 32
+// heads of 128 x 128 in 3.07, 2.78, 2.65, 2.71 and 2.99 ms, 16384 tokens in 781, 714, 673, 699 and 749 us, 4 x 8192
+// tokens in 1.10, 1.17, 1.05, 1.10 and 1.14 ms.
 constexpr size_t kSegBytes = size_t{96} << 20;
 
 inline Plan make_fwd_plan(int64_t batch, int64_t seqlen, int64_t hk, int64_t heads, int64_t dk, int64_t dv) {
