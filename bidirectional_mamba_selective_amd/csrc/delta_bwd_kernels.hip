@@ -396,7 +396,7 @@ __global__ __launch_bounds__(512, 2) void k_delta_grads(GradArgs a) {
   __shared__ __align__(16) uint16_t sQ[C * kRow], sK[C * kRow];
   __shared__ float sP[C * kPitch];
   __shared__ __align__(16) float sHi[C], sLo[C], sEg[C], sKeep[C];
-  __shared__ float sS0[2][C], sS1[2][C], sDb[C], sTurn[C], sAcc[8][C], sDot[8];
+  __shared__ float sS0[2][C], sS1[2][C], sDb[C], sAcc[8][C], sDot[8];
   Slices<DK>& sl = *reinterpret_cast<Slices<DK>*>(shared);
   Scores& sc = *reinterpret_cast<Scores*>(shared);
   const int lane = threadIdx.x & 63, l16 = lane & 15, q4 = lane >> 4;
@@ -599,8 +599,7 @@ __global__ __launch_bounds__(512, 2) void k_delta_grads(GradArgs a) {
       // sums of s over i >= t (as prefix sums of the reversed row) and of e over j < t
       const float from = prefix_sum(sS0[0][C - 1 - lane] + sS0[1][C - 1 - lane]);
       const float before = prefix_sum(lane > 0 ? sS1[0][lane - 1] + sS1[1][lane - 1] : 0.0f);
-      sTurn[C - 1 - lane] = from;
-      float dg = sTurn[lane] + before, all = 0.0f;
+      float dg = __shfl(from, C - 1 - lane) + before, all = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) dg += sAcc[i][lane], all += sDot[i];
       dg = fmaf(sEg[C - 1], all, dg);
