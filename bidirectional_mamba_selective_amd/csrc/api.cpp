@@ -759,7 +759,7 @@ int bimamba_proj_fp8(const void* x, const float* x_scales, const void* w, const 
 // ---- Gated delta rule ----
 
 static int delta_check_shape(int64_t batch, int64_t seqlen, int64_t hk, int64_t heads, int64_t dk, int64_t dv,
-                             int io_dtype) {
+                             int io_dtype, bool grad) {
   if (batch <= 0 || seqlen <= 0 || hk <= 0 || heads <= 0 || dk <= 0 || dv <= 0) return BIMAMBA_ERR_INVALID_ARGUMENT;
   if (heads % hk != 0) return BIMAMBA_ERR_INVALID_ARGUMENT;
   if (io_dtype != BIMAMBA_BF16) return BIMAMBA_ERR_UNSUPPORTED;
@@ -768,8 +768,8 @@ static int delta_check_shape(int64_t batch, int64_t seqlen, int64_t hk, int64_t 
   // eight heads, in a grid of fewer than 2^32 threads
   if (batch > 65535 || heads > 65535 || seqlen > INT32_MAX / 2) return BIMAMBA_ERR_UNSUPPORTED;
   if (static_cast<double>(batch) * heads > 1.0e6) return BIMAMBA_ERR_UNSUPPORTED;
-  // a chunk, head and batch element per workgroup of 256 threads
-  if (static_cast<double>((seqlen + 63) / 64) * 256 > 4.0e9) return BIMAMBA_ERR_UNSUPPORTED;
+  // chunks are a grid dimension too, of workgroups of 256 threads (forward) or 512 (gradients), again below 2^32 threads
+  if (static_cast<double>((seqlen + 63) / 64) * (grad ? 512 : 256) > 4.0e9) return BIMAMBA_ERR_UNSUPPORTED;
   return BIMAMBA_OK;
 }
 
@@ -782,7 +782,8 @@ static int delta_check_args(const void* q, const void* k, const void* v, const v
 
 size_t bimamba_delta_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads_k, int64_t nheads,
                                          int64_t headdim_k, int64_t headdim_v) {
-  if (delta_check_shape(batch, seqlen, nheads_k, nheads, headdim_k, headdim_v, BIMAMBA_BF16) != BIMAMBA_OK) return 0;
+  if (delta_check_shape(batch, seqlen, nheads_k, nheads, headdim_k, headdim_v, BIMAMBA_BF16, false) != BIMAMBA_OK)
+    return 0;
   return bimamba::delta::make_fwd_plan(batch, seqlen, nheads_k, nheads, headdim_k, headdim_v).total;
 }
 
@@ -790,7 +791,7 @@ int bimamba_delta_fwd(const void* q, const void* k, const void* v, const void* d
                       const float* dt_bias, const float* h_in, float* h_out, void* out, int64_t batch, int64_t seqlen,
                       int64_t nheads_k, int64_t nheads, int64_t headdim_k, int64_t headdim_v, float scale, int io_dtype,
                       uint32_t flags, void* workspace, size_t workspace_bytes, hipStream_t stream) {
-  int s = delta_check_shape(batch, seqlen, nheads_k, nheads, headdim_k, headdim_v, io_dtype);
+  int s = delta_check_shape(batch, seqlen, nheads_k, nheads, headdim_k, headdim_v, io_dtype, false);
   if (s != BIMAMBA_OK) return s;
   s = delta_check_args(q, k, v, dt, A, b, scale, flags);
   if (s != BIMAMBA_OK) return s;
@@ -819,7 +820,8 @@ int bimamba_delta_fwd(const void* q, const void* k, const void* v, const void* d
 
 size_t bimamba_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads_k, int64_t nheads,
                                          int64_t headdim_k, int64_t headdim_v) {
-  if (delta_check_shape(batch, seqlen, nheads_k, nheads, headdim_k, headdim_v, BIMAMBA_BF16) != BIMAMBA_OK) return 0;
+  if (delta_check_shape(batch, seqlen, nheads_k, nheads, headdim_k, headdim_v, BIMAMBA_BF16, true) != BIMAMBA_OK)
+    return 0;
   return bimamba::delta::make_bwd_plan(batch, seqlen, nheads_k, nheads, headdim_k, headdim_v).total;
 }
 
@@ -829,7 +831,7 @@ int bimamba_delta_bwd(const void* dout, const void* q, const void* k, const void
                       int64_t seqlen, int64_t nheads_k, int64_t nheads, int64_t headdim_k, int64_t headdim_v,
                       float scale, int io_dtype, uint32_t flags, void* workspace, size_t workspace_bytes,
                       hipStream_t stream) {
-  int s = delta_check_shape(batch, seqlen, nheads_k, nheads, headdim_k, headdim_v, io_dtype);
+  int s = delta_check_shape(batch, seqlen, nheads_k, nheads, headdim_k, headdim_v, io_dtype, true);
   if (s != BIMAMBA_OK) return s;
   s = delta_check_args(q, k, v, dt, A, b, scale, flags);
   if (s != BIMAMBA_OK) return s;

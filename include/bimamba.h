@@ -479,7 +479,7 @@ int bimamba_proj_fp8(const void* x, const float* x_scales, const void* w, const 
  * (a padded place: with finite q, k, v there); other non-finite values make the results of their batch element and head
  * non-finite from the 64-token chunk on in which they stand.
  * Supported: io_dtype BIMAMBA_BF16 (q, k, v, dt, b, out), headdim_k and headdim_v 64 or 128, nheads a multiple of
- * nheads_k, batch and nheads at most 65535, batch * nheads at most 10^6.  q, k, v, out, h_in, h_out 16-byte aligned, dt
+ * nheads_k, batch and nheads at most 65535, batch * nheads at most 10^6, seqlen at most 10^9.  q, k, v, out, h_in, h_out 16-byte aligned, dt
  * and b 2, A and dt_bias 4.  States and all sums are carried at fp32 accuracy.
  * Up to 16 tokens need no workspace (bimamba_delta_fwd_workspace_bytes returns 0, workspace may be NULL); otherwise it is
  * 256-byte aligned and its contents on entry are ignored.  No output may overlap an input (h_out equal to h_in excepted),
@@ -499,7 +499,7 @@ int bimamba_delta_fwd(const void* q, const void* k, const void* v, const void* d
  * db is 0 where beta is below 2^-60.  ddt_bias and dh_in may be NULL (not written); they may be asked for also where
  * dt_bias or h_in is NULL.  dh_in may
  * equal dh_out.  All sums run in a fixed order: two calls on the same inputs give the same bits.  Shapes, types, flags and
- * alignment are as for bimamba_delta_fwd; workspace 256-byte aligned, contents ignored on entry.  No output may overlap
+ * alignment are as for bimamba_delta_fwd, seqlen at most 5 * 10^8; workspace 256-byte aligned, contents ignored on entry.  No output may overlap
  * an input (dh_in equal to dh_out excepted), another output or the workspace. */
 size_t bimamba_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads_k, int64_t nheads,
                                          int64_t headdim_k, int64_t headdim_v);

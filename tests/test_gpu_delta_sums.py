@@ -54,7 +54,7 @@ def case(kind, L, dk, dv, rev):
         c = 1 / (1 + np.exp(-b))
     else:                     # scores that carry a decay, corrections v
         b = np.array([40.0, 40.0])
-        dt = 0.375
+        dt = 1.78125  # of such steps' decays one of the farthest from 17 bits
         inp["dt"][0, t1] = dt
         c = np.array([np.exp(-np.logaddexp(dt, 0.0)), 1.0])
     v = near(c[0], c[1], dv, L)
