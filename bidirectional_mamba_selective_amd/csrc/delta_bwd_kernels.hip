@@ -607,7 +607,8 @@ __global__ __launch_bounds__(512, 2) void k_delta_grads(GradArgs a) {
       if (real) {
         const float x = bf(own_dt) + (a.dt_bias ? a.dt_bias[h] : 0.0f);
         const float ddt = dg * a.A[h] * sigmoid_f32(x);
-        pa = dg * softplus_f32(x);
+        // (0 where nothing crosses the token: its step may be infinite there)
+        pa = dg == 0.0f ? 0.0f : dg * softplus_f32(x);
         pb = ddt;
         bf16_t o;
         from_f32(ddt, &o);

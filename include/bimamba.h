@@ -475,9 +475,12 @@ int bimamba_proj_fp8(const void* x, const float* x_scales, const void* w, const 
  * direction's first and after its last token (the cache of block decoding: a block, or a single token, is a call
  * with both; h_out may equal h_in).  dt_bias, h_in and h_out may be NULL (zeros; not written).
  * The layer is meant for A <= 0 and keys of about unit length; the states grow without bound otherwise.  Decays below
- * e^-256 per token count as e^-256 (zero in fp32).  b = -inf and dt = -inf are allowed and make a token that leaves the state as it is
- * (a padded place: with finite q, k, v there); other non-finite values make the results of their batch element and head
- * non-finite from the 64-token chunk on in which they stand.
+ * e^-256 per token count as e^-256 (zero in fp32).  Infinities in the gates mean their limits, where q, k and v are
+ * finite: dt = -inf no decay (delta = 0), b = -inf no correction (beta = 0), both together a padded place, a token that
+ * leaves the state as it is; dt = +inf with A < 0 a cleared state (a = 0), b = +inf beta = 1.  The gradients of such gates
+ * are 0.  A and dt_bias are finite.  Any other non-finite value makes results non-finite, of its batch element and the
+ * heads that read it only: in q its own token's out; in v its column, and in k, dt (NaN) or b (NaN) the whole head, of the
+ * state and of out, from the 64-token run on in which it stands (from its token on in calls of up to 16 tokens).
  * Supported: io_dtype BIMAMBA_BF16 (q, k, v, dt, b, out), headdim_k and headdim_v 64 or 128, nheads a multiple of
  * nheads_k, batch and nheads at most 65535, batch * nheads at most 10^6, seqlen at most 10^9.  q, k, v, out, h_in, h_out 16-byte aligned, dt
  * and b 2, A and dt_bias 4.  States and all sums are carried at fp32 accuracy.
