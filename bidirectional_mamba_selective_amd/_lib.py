@@ -80,6 +80,10 @@ def load() -> ctypes.CDLL:
         return _lib
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m bidirectional_mamba_selective_amd.build`")
+    try:
+        _torch()  # first, so that the library binds to torch's HIP runtime: loaded before it, it brings one of its own,
+    except ImportError:  # to which torch's streams mean nothing (without torch, sizes and checks still work)
+        pass
     lib = ctypes.CDLL(LIB_PATH)
     vp, i64, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
     lib.bimamba_version.restype = ctypes.c_int
