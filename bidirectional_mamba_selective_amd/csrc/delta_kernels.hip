@@ -579,7 +579,7 @@ __global__ __launch_bounds__(SAVE ? 256 : 512, SAVE ? 1 : 2) void k_delta_walk(W
   }
 }
 
-// Up to kStepMax tokens, one after the other, all in fp32: a wavefront per 32 columns of a head's state, which it holds in
+// A few tokens (token_by_token), one after the other, all in fp32: a wavefront per 32 columns of a head's state, which it holds in
 // registers (8 lanes x 4 columns, an eighth of the rows each).  One token is bound by HBM, each state being read and
 // written once: 16 x 32 heads of 128 x 128 in 12.9 us, 5.2 TB/s; further tokens by the two sums over the rows that follow
 // from one another (0.97 us a token at 32 heads).

@@ -11,10 +11,21 @@ namespace bimamba {
 namespace delta {
 
 constexpr int64_t kC = 64;            // tokens per chunk
-// Tokens up to which the forward pass goes token by token, without a workspace.  That takes 0.97 us a token for 32 heads
-// of 128 x 128 and 3.1 us for 512, by chunks the call takes as long for 1 token as for 64: 8 tokens 11.1 and 14.3 us (by
-// chunks), 16 tokens 19.0 and 14.4, for 512 heads 37 and 51, 24 tokens 49 and 52, 32 tokens 62 and 53.
-constexpr int64_t kStepMax = 16;
+// Tokens up to which the forward pass goes token by token, without a workspace: 16, and 24 where the states hold 2^22
+// values.  By chunks a call takes as long for 1 token as for 64 (token by token | by chunks, us; batch x heads of
+// 128 x 128 unless given):
+//    8 tokens:  32: 11.6 | 14.9   512: 24.5 | 54.5
+//   16 tokens:  32: 19.4 | 14.9   128: 21.0 | 22.8   256: 23.3 | 33.4   512: 37.0 | 55.3   of 64 x 64: 32: 15.0 | 13.6
+//   24 tokens: 128: 28.6 | 23.2   256: 31.0 | 33.8   512: 49.6 | 56.1   of 64 x 64: 256: 22.1 | 18.2, 1024: 33.8 | 41.0
+//   28 tokens: 256: 34.8 | 34.2   512: 55.5 | 56.6   1024: 95.1 | 98.2
+// With few heads chunks are the faster way from 12 tokens on, by up to 4.5 us at 16: a decoding block of 16 tokens gets by
+// without a workspace whatever its heads.
+constexpr int64_t kStepTokens = 16, kStepTokensWide = 24, kStepWide = int64_t{1} << 22;
+
+inline bool token_by_token(int64_t batch, int64_t seqlen, int64_t heads, int64_t dk, int64_t dv) {
+  return seqlen <= (batch * heads * dk * dv >= kStepWide ? kStepTokensWide : kStepTokens);
+}
+
 constexpr size_t kFragBytes = 1024;   // one matrix operand of 16 x 32 bf16 values, 16 bytes a lane
 constexpr int64_t kTriFrags = 6;      // operands that a triangular 64 x 64 matrix has (of 8; the others are zero)
 constexpr int64_t kGateFloats = 320;  // per (head, chunk): five rows of 64, see k_delta_prep
@@ -65,7 +76,7 @@ inline Plan make_fwd_plan(int64_t batch, int64_t seqlen, int64_t hk, int64_t hea
   Plan p{};
   p.nchunk = (seqlen + kC - 1) / kC;
   p.tiles = walk_tiles(batch * heads, dv);
-  if (seqlen <= kStepMax) return p;
+  if (token_by_token(batch, seqlen, heads, dk, dv)) return p;
   const Layout l = make_layout(dk, false);
   const size_t per_chunk = static_cast<size_t>(batch) * (heads * l.bytes + hk * l.key_bytes);
   int64_t seg = static_cast<int64_t>(kSegBytes / per_chunk);

@@ -138,7 +138,7 @@ struct DeltaGrads {
   float* dh_in;     // null: not written
 };
 
-// Forward: token by token up to kStepMax tokens (no workspace), by chunks above.
+// Forward: token by token (no workspace) where token_by_token says so, by chunks otherwise.
 hipError_t launch_delta_step(const DeltaArgs& a, hipStream_t stream);
 hipError_t launch_delta_fwd(const DeltaArgs& a, const Plan& p, void* workspace, hipStream_t stream);
 hipError_t launch_delta_bwd(const DeltaArgs& a, const DeltaGrads& g, const Plan& p, void* workspace,

@@ -480,13 +480,13 @@ int bimamba_proj_fp8(const void* x, const float* x_scales, const void* w, const 
  * leaves the state as it is; dt = +inf with A < 0 a cleared state (a = 0), b = +inf beta = 1.  The gradients of such gates
  * are 0.  A and dt_bias are finite.  Any other non-finite value makes results non-finite, of its batch element and the
  * heads that read it only: in q its own token's out; in v its column, and in k, dt (NaN) or b (NaN) the whole head, of the
- * state and of out, from the 64-token run on in which it stands (from its token on in calls of up to 16 tokens).
+ * state and of out, from the 64-token run on in which it stands (from its token on in a call without a workspace).
  * Supported: io_dtype BIMAMBA_BF16 (q, k, v, dt, b, out), headdim_k and headdim_v 64 or 128, nheads a multiple of
  * nheads_k, batch and nheads at most 65535, batch * nheads at most 10^6, seqlen at most 10^9.  q, k, v, out, h_in, h_out 16-byte aligned, dt
  * and b 2, A and dt_bias 4.  States and all sums are carried at fp32 accuracy.
- * Up to 16 tokens need no workspace (bimamba_delta_fwd_workspace_bytes returns 0, workspace may be NULL); otherwise it is
- * 256-byte aligned and its contents on entry are ignored.  No output may overlap an input (h_out equal to h_in excepted),
- * another output or the workspace. */
+ * Up to 16 tokens, or 24 where the states hold at least 2^22 values, need no workspace (bimamba_delta_fwd_workspace_bytes
+ * returns 0, workspace may be NULL); otherwise it is 256-byte aligned and its contents on entry are ignored.  No output may
+ * overlap an input (h_out equal to h_in excepted), another output or the workspace. */
 size_t bimamba_delta_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads_k, int64_t nheads,
                                          int64_t headdim_k, int64_t headdim_v);
 
