@@ -366,7 +366,7 @@ struct Slices {
 };
 
 struct Scores {
-  uint16_t d1[2][C * C], d1t[2][C * C], d2[2][C * C], d2t[2][C * C];
+  uint16_t d1[3][C * C], d1t[3][C * C], d2[3][C * C], d2t[3][C * C];
 };
 
 __device__ __forceinline__ void put_slice(uint16_t* to, int size, int at, f32x8 v) {
@@ -384,10 +384,10 @@ __device__ __forceinline__ void get_slice(const uint16_t* from, int size, int at
 // Eight wavefronts: wavefront w + 4 c takes the chunk's tokens 16 w .. + 15 and, of the tokens or columns that it meets
 // them with, the tiles of parity c.  The contractions over the value head's columns go 32 columns at a time: every value of
 // the states, U and dR is loaded once, a slice ahead, and split once into the three parts that all wavefronts read from
-// LDS.  What ends in an fp32 result (the sums of P, s and e) is formed from all three parts, D1 and D2 as operands of the
-// bf16 results from two.  Bound by the vector instructions that split values and the waits between slices at one
-// workgroup a compute unit (two need 128 registers a lane): 128 chunks of 32 heads of 128 x 128 in 568 us, of which
-// the 0.8 GB of states, U and dR take 160; 611 with the prefix sums by shuffles.
+// LDS.  All of these, and D1 and D2 as operands of the products within the chunk, keep their three parts.  Bound by the
+// vector instructions that split values and the waits between slices at one workgroup a compute unit, which is what the
+// LDS holds (151 KB with keys of 128, 135 with 64; the registers, some 250 a lane, allow no second one either): 128
+// chunks of 32 heads of 128 x 128 in 584 us, of which the 0.8 GB of states, U and dR take 160.
 template <int DK, int DV>
 __global__ __launch_bounds__(512, 2) void k_delta_grads(GradArgs a) {
   constexpr int KS = DK / 32, ST = DK / 64, VS = DV / 32, KT = DK / 32, kRow = DK + 8, kPitch = C + 1;
@@ -516,11 +516,11 @@ __global__ __launch_bounds__(512, 2) void k_delta_grads(GradArgs a) {
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) sP[(16 * w + 4 * q4 + r) * kPitch + 16 * j + l16] = pr[r];
-      u32x2 p1[2], p2[2];
+      u32x2 p1[3], p2[3];
       split4(d1[jj], p1);
       split4(d2[jj], p2);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 3; ++i) {
         write4<C>(sc.d1t[i], 16 * j + l16, 16 * w + 4 * q4, p1[i]);
         write4<C>(sc.d2t[i], 16 * j + l16, 16 * w + 4 * q4, p2[i]);
 #pragma unroll
@@ -561,9 +561,9 @@ __global__ __launch_bounds__(512, 2) void k_delta_grads(GradArgs a) {
     const __amdgpu_buffer_rsrc_t keys = record(key, a.lay.key_bytes);
 #pragma unroll 1
     for (int s = 0; s < 2; ++s) {
-      bf16x8 d1[2], d2[2], d1t[2], d2t[2];
+      bf16x8 d1[3], d2[3], d1t[3], d2t[3];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 3; ++i) {
         d1[i] = read8<C>(sc.d1[i], 16 * w + l16, 32 * s + 8 * q4);
         d2[i] = read8<C>(sc.d2[i], 16 * w + l16, 32 * s + 8 * q4);
         d1t[i] = read8<C>(sc.d1t[i], 16 * w + l16, 32 * s + 8 * q4);

@@ -81,3 +81,49 @@ def test_cancelling_terms_of_out(kind, L, dk, dv, rev):
     worst = float(np.max(np.abs(got - want) / allow))
     say(f"{kind} L {L} {dk} x {dv}: worst element at {worst:.3f} of its bound")
     assert worst <= 1.0
+
+
+def opposite(a, r):
+    """-a, but for one place, where both are about 2^-6 and the other is 2^-7 larger: their sum is about 2^-13."""
+    a, c = a.copy(), r.integers(0, a.shape[-1])
+    a[..., c] = 2.0 ** -6 * (1 + r.integers(0, 64) / 128)
+    b = -a
+    b[..., c] *= 1 + 2.0 ** -7
+    b = inputs.round_to(b.astype(np.float32), "bf16")
+    return a, b
+
+
+@pytest.mark.parametrize("rev", [False, True])
+@pytest.mark.parametrize("L,dk,dv", [(64, 64, 64), (64, 128, 128), (64, 64, 128), (100, 128, 64)])
+def test_cancelling_terms_of_the_gradients_of_q_and_k(L, dk, dv, rev):
+    """dq of a token whose two terms D1 k nearly cancel (two orthogonal keys with one coordinate alike, values nearly
+    opposite); dk of a token whose terms D1 q, two and two, nearly cancel (one query, gradients nearly opposite).  A score
+    is a sum of dv products: 2^-22 of their magnitudes, which 24-bit operands keep; 17 bits would be off by 2^-17 of the
+    score, some 2^3 half steps of the difference."""
+    import bidirectional_mamba_selective_amd as bm
+    import oracle
+
+    r, scale = np.random.default_rng(dk + dv), 0.125
+    rnd = lambda *s: inputs.round_to(r.standard_normal(s).astype(np.float32), "bf16")  # noqa: E731
+    at = (lambda t: L - 1 - t) if rev else (lambda t: t)
+    n = 10
+    inp = tokens(L, dk, dv)
+    dout = np.zeros((1, L, 1, dv), np.float32)
+    v0, v1 = opposite(rnd(dv), r)
+    for t, key, v in ((T0, (0.5, 0.5), v0), (T1, (0.5, -0.5), v1)):
+        inp["k"][0, at(t), 0, :2] = key
+        inp["v"][0, at(t), 0] = v
+        inp["b"][0, at(t)] = 40
+    pairs = [(TQ + 2 * m, TQ + 2 * m + 1) for m in range(n)]
+    for m, (t0, t1) in enumerate(pairs):
+        dout[0, at(t0), 0], dout[0, at(t1), 0] = opposite(rnd(dv), r)
+        inp["q"][0, [at(t0), at(t1)], 0, 2 + m] = 1
+    dev = {x: to_dev(y, "bf16") if x in ("q", "k", "v", "dt", "b") else f32_dev(y) for x, y in inp.items()}
+    g = bm.bimamba_delta_bwd(to_dev(dout, "bf16"), **dev, scale=scale, flags=bm.FLAG_REV_ONLY if rev else bm.FLAG_FWD_ONLY)
+    want = oracle.delta_bwd(dout, inp, scale=scale, rev=rev)
+    for m, (t0, t1) in enumerate(pairs):
+        terms = scale * float((np.abs(dout[0, at(t0), 0]) * np.abs(v0)).sum())
+        for name, t, c, size in (("q", t0, 0, 0.5), ("q", t1, 0, 0.5), ("k", T0, 2 + m, 1.0), ("k", T1, 2 + m, 1.0)):
+            got, w = to_host64(g[name])[0, at(t), 0, c], want[name][0, at(t), 0, c]
+            allow = 2.0 ** -8 * abs(w) + 2.0 ** -22 * 2 * size * terms
+            assert abs(got - w) <= allow, (name, t, got, w, abs(got - w) / allow)
