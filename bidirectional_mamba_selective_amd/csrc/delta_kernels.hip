@@ -311,7 +311,7 @@ __device__ __forceinline__ bool place(int64_t slices, int64_t rows, int64_t* row
 //   K^T U: through LDS, the wavefront's rows of S
 // What bounds it is the latency of one chunk's chain, which no other chunk can shorten: three LDS round trips of 140 to 185
 // cycles, three barriers, the products between them and the three-part splits; 2.0 us a chunk at 32 heads of 128 x 128
-// (57 chunks in 115 us; 65536 tokens, with k_delta_prep, in 2.65 ms, where the inputs' bytes take 0.43).  16 columns
+// (57 chunks in 115 us; 65536 tokens, with k_delta_prep, in 2.67 ms, where the inputs' bytes take 0.43).  16 columns
 // a workgroup put one on every compute unit at 32 heads.  The whole chain in the registers of one wavefront, without
 // barriers, took 166 us where this took 130: its vector instructions, no longer spread over four SIMDs, then set the
 // pace.
@@ -579,10 +579,11 @@ __global__ __launch_bounds__(SAVE ? 256 : 512, SAVE ? 1 : 2) void k_delta_walk(W
   }
 }
 
-// A few tokens (token_by_token), one after the other, all in fp32: a wavefront per 32 columns of a head's state, which it holds in
-// registers (8 lanes x 4 columns, an eighth of the rows each).  One token is bound by HBM, each state being read and
-// written once: 16 x 32 heads of 128 x 128 in 12.9 us, 5.2 TB/s; further tokens by the two sums over the rows that follow
-// from one another (0.97 us a token at 32 heads).
+// A few tokens (token_by_token), one after the other, all in fp32: a wavefront per 32 columns of a head's state, which it
+// holds in registers (8 lanes x 4 columns, an eighth of the rows each).  One token is bound by the states, each read and
+// written once: 16 x 32 heads of 128 x 128 (67 MB) in 14.8 us from memory (16 such calls on states of their own in turn,
+// 4.5 TB/s), 12.9 us where the last-level cache holds them; further tokens by the two sums over the rows that follow from
+// one another (0.97 us a token at 32 heads).
 struct StepArgs {
   const uint16_t* q;
   const uint16_t* k;

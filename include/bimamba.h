@@ -454,8 +454,10 @@ int bimamba_adaln_bwd(const void* dout, const void* dres, const void* h, const v
  * x and x_scales are what bimamba_adaln_fwd_fp8 writes (any row count: a batch of sequences, a block, one token); w is
  * quantised once, one scale for each 128 x 128 weights (n / 128 rounded down; the last row of scales serves the rest of
  * the outputs).  Products are exact and out is rounded to nearest even once; fp32 results sum in fp32, bf16 results as the
- * 8-bit matrix instructions do, which drop low bits beside large terms (within 2^-12 of the terms' magnitudes, 1.4e-5
- * normwise, before the rounding to bf16's 2^-9).
+ * 8-bit matrix instructions do, which drop low bits beside large terms (a block's sum within 2^-12 of its terms'
+ * magnitudes; 1.5e-5 of the results' rms for operands of one scale, any d_in, before the rounding to bf16's 2^-9).
+ * The two scales of a block are multiplied first, in fp32: that product has to be a normal number (or its block's sum is
+ * lost: 0, or not finite).
  *   x: [rows, d_in], w: [d_out, d_in], one byte a value; x_scales: [rows, d_in / 128] fp32;
  *   w_scales: [(d_out + 127) / 128, d_in / 128] fp32; out: [rows, d_out], out_dtype BIMAMBA_BF16 or BIMAMBA_F32.
  * Supported: d_in a multiple of 128, d_out of 8, both at most 2^22, 1 <= rows <= 2^31, and at most 2^23 tiles of 128 rows
@@ -499,7 +501,9 @@ int bimamba_delta_fwd(const void* q, const void* k, const void* v, const void* d
  * h_out (NULL = 0).  Nothing of the forward call is needed: everything is recomputed from its inputs.
  *   dq, dk, dv, ddt, db: like their inputs (bf16, rounded once; dq and dk summed over the heads that share them);
  *   dA, ddt_bias [nheads] fp32, summed over batch and tokens; dh_in: the gradient of h_in.
- * db is 0 where beta is below 2^-60.  ddt_bias and dh_in may be NULL (not written); they may be asked for also where
+ * db is 0 where beta is below 2^-60, and loses bits where beta^2 times the gradients falls below fp32's normal numbers.
+ * The workspace holds every 64-token run's operands and states: 1.2 GB for 8192 tokens of 32 heads of 128 x 128, in
+ * proportion to tokens and heads.  ddt_bias and dh_in may be NULL (not written); they may be asked for also where
  * dt_bias or h_in is NULL.  dh_in may
  * equal dh_out.  All sums run in a fixed order: two calls on the same inputs give the same bits.  Shapes, types, flags and
  * alignment are as for bimamba_delta_fwd, seqlen at most 5 * 10^8; workspace 256-byte aligned, contents ignored on entry.  No output may overlap
