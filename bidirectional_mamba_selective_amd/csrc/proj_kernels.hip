@@ -6,9 +6,10 @@
 // bf16 results take a block of 128 inputs in one v_mfma_f32_16x16x128_f8f6f4.  Its adder drops low bits of small products
 // beside large ones: sums of N(0, 1) operands come out 1.4e-5 off normwise (1.3e-5 of the terms' magnitudes at most on
 // single ones; 1.5e-5 of the rms for 128 to 16384 inputs), the same as with the older 8-bit instructions.  Next to the
-// result's own rounding, 2^-9, it moves the distance to the exact product in the fifth digit (1.65878e-3 and 1.65871e-3
-// from fp32 sums, 32 x 8056 x 1920), for twice the rate of bf16 operands.  fp32 results are to be better than that: there the operands are widened to bf16, which holds every e4m3 value,
-// and take four v_mfma_f32_16x16x32_bf16, whose sums are fp32 ones (1e-7), at half the rate.
+// result's own rounding, up to 2^-8, it moves the distance to the exact product in the fifth digit (1.65878e-3 and
+// 1.65871e-3 from fp32 sums, 32 x 8056 x 1920), for twice the rate of bf16 operands.  fp32 results are to be better than
+// that: there the operands are widened to bf16, which holds every e4m3 value, and take four v_mfma_f32_16x16x32_bf16, whose
+// sums are fp32 ones (1e-7), at half the rate.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -411,8 +411,8 @@ int bimamba_adaln_fwd(const void* x, const void* branch, const float* post_weigh
 /* bimamba_adaln_fwd with out in 8 bits, as the projection that follows it reads it (bimamba_proj_fp8): with
  * y the value that bimamba_adaln_fwd rounds to out, and for each row and each run of 128 columns
  *   scale = max(max |y|, 2^-100) / 448,   out = y / scale rounded to nearest even e4m3
- * (OCP e4m3: 448 is its largest value; both divisions are fp32 ones, correctly rounded).  With beta NULL and RMS_NORM this is the
- * root-mean-square norm behind the residual's addition.
+ * (OCP e4m3: 448 is its largest value; both divisions are fp32 ones, correctly rounded).  With beta NULL and RMS_NORM this
+ * is the root-mean-square norm behind the residual's addition.
  *   out: [batch, seqlen, d_model], one byte a value; scales: [batch, seqlen, d_model / 128] fp32.
  * A NaN makes out NaN where bimamba_adaln_fwd's would be one; the scales pass over it.
  * d_model must be a multiple of 128; everything else is as for bimamba_adaln_fwd, whose backward pass is also this one's
@@ -455,7 +455,7 @@ int bimamba_adaln_bwd(const void* dout, const void* dres, const void* h, const v
  * quantised once, one scale for each 128 x 128 weights (n / 128 rounded down; the last row of scales serves the rest of
  * the outputs).  Products are exact and out is rounded to nearest even once; fp32 results sum in fp32, bf16 results as the
  * 8-bit matrix instructions do, which drop low bits beside large terms (a block's sum within 2^-12 of its terms'
- * magnitudes; 1.5e-5 of the results' rms for operands of one scale, any d_in, before the rounding to bf16's 2^-9).
+ * magnitudes; 1.5e-5 of the results' rms for operands of one scale, any d_in), before the rounding to bf16, up to 2^-8.
  * The two scales of a block are multiplied first, in fp32: that product has to be a normal number (or its block's sum is
  * lost: 0, or not finite).
  *   x: [rows, d_in], w: [d_out, d_in], one byte a value; x_scales: [rows, d_in / 128] fp32;
@@ -484,8 +484,8 @@ int bimamba_proj_fp8(const void* x, const float* x_scales, const void* w, const 
  * heads that read it only: in q its own token's out; in v its column, and in k, dt (NaN) or b (NaN) the whole head, of the
  * state and of out, from the 64-token run on in which it stands (from its token on in a call without a workspace).
  * Supported: io_dtype BIMAMBA_BF16 (q, k, v, dt, b, out), headdim_k and headdim_v 64 or 128, nheads a multiple of
- * nheads_k, batch and nheads at most 65535, batch * nheads at most 10^6, seqlen at most 10^9.  q, k, v, out, h_in, h_out 16-byte aligned, dt
- * and b 2, A and dt_bias 4.  States and all sums are carried at fp32 accuracy.
+ * nheads_k, batch and nheads at most 65535, batch * nheads at most 10^6, seqlen at most 10^9.  q, k, v, out, h_in, h_out
+ * 16-byte aligned, dt and b 2, A and dt_bias 4.  States and all sums are carried at fp32 accuracy.
  * Up to 16 tokens, or 24 where the states hold at least 2^22 values, need no workspace (bimamba_delta_fwd_workspace_bytes
  * returns 0, workspace may be NULL); otherwise it is 256-byte aligned and its contents on entry are ignored.  No output may
  * overlap an input (h_out equal to h_in excepted), another output or the workspace. */
@@ -502,12 +502,11 @@ int bimamba_delta_fwd(const void* q, const void* k, const void* v, const void* d
  *   dq, dk, dv, ddt, db: like their inputs (bf16, rounded once; dq and dk summed over the heads that share them);
  *   dA, ddt_bias [nheads] fp32, summed over batch and tokens; dh_in: the gradient of h_in.
  * db is 0 where beta is below 2^-60, and loses bits where beta^2 times the gradients falls below fp32's normal numbers.
- * The workspace holds every 64-token run's operands and states: 1.2 GB for 8192 tokens of 32 heads of 128 x 128, in
- * proportion to tokens and heads.  ddt_bias and dh_in may be NULL (not written); they may be asked for also where
- * dt_bias or h_in is NULL.  dh_in may
- * equal dh_out.  All sums run in a fixed order: two calls on the same inputs give the same bits.  Shapes, types, flags and
- * alignment are as for bimamba_delta_fwd, seqlen at most 5 * 10^8; workspace 256-byte aligned, contents ignored on entry.  No output may overlap
- * an input (dh_in equal to dh_out excepted), another output or the workspace. */
+ * ddt_bias and dh_in may be NULL (not written); they may be asked for also where dt_bias or h_in is NULL.  dh_in may equal
+ * dh_out.  All sums run in a fixed order: two calls on the same inputs give the same bits.  Shapes, types, flags and
+ * alignment are as for bimamba_delta_fwd, seqlen at most 5 * 10^8.  The workspace, 256-byte aligned, contents ignored on
+ * entry, holds every 64-token run's operands and states: 1.2 GB for 8192 tokens of 32 heads of 128 x 128, in proportion to
+ * tokens and heads.  No output may overlap an input (dh_in equal to dh_out excepted), another output or the workspace. */
 size_t bimamba_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads_k, int64_t nheads,
                                          int64_t headdim_k, int64_t headdim_v);
 
